@@ -293,7 +293,7 @@ def _plain_extend(s):
     if s["parents"] is None:
         return out + [torch.where(real, row, -1).int()]
     sees = _sees(s["parents"])
-    return out + [torch.where(real, L[:, None] + sees.sum(-1) - 1, -1).int(), _pack(sees)]
+    return out + [torch.where(real, L[:, None] + sees.sum(-1) - 1, -1).int(), _pack(sees & real[:, :, None])]
 
 
 def _rotate(x, cs, interleaved):
@@ -464,7 +464,7 @@ def _exact_extend(s):
             top -= 1
             table[b][p] = stack[top]
         for t in range(q):
-            up, depth = t, -1
+            up, depth = t if t < new[b] else -1, -1
             while parents is not None and up >= 0:
                 w = masks[b][t][up // 32] | 1 << up % 32
                 masks[b][t][up // 32] = w
