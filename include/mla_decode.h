@@ -53,7 +53,8 @@ typedef enum mla_status {
     MLA_ERR_WORKSPACE = -4,     /* workspace too small for (batch, q_len, num_heads, num_sms) */
     MLA_ERR_CUDA = -5,          /* a CUDA runtime/driver call failed (see mla_last_cuda_error) */
     MLA_ERR_TIMEOUT = -6,       /* device status: a bounded wait inside a kernel ran out */
-    MLA_ERR_BLOCK_TABLE = -7    /* device status: a block-table entry was outside [0, kv_rows) */
+    MLA_ERR_BLOCK_TABLE = -7,   /* device status: a block-table entry was outside [0, kv_rows) */
+    MLA_ERR_PAGES = -8          /* device status: fewer free pages than the new tokens need */
 } mla_status;
 
 enum {
@@ -178,6 +179,128 @@ MLA_API int mla_decode_fwd_fp8(const void *q, const void *kv8, const float *kv_s
                        const int32_t *q_lens, const int32_t *block_table, int batch, int q_len, int num_heads,
                        int64_t kv_rows, int max_blocks, float softmax_scale, int causal, void *o, float *lse,
                        void *workspace, size_t workspace_bytes, int num_sms, unsigned flags, void *stream);
+
+/*
+ * Tree decode: mla_decode_fwd_ragged for drafts that form a tree (speculative verify over several
+ * candidate continuations), where the pages decode one token per forward.  Sequence b's
+ * n = q_lens[b] (or q_len) new tokens are its last n cache rows; token t sees every row
+ * j < L_b - n ahead of them and, of the new rows, L_b - n + u for each u whose bit is set in its
+ * mask: bit u % 32 of word u / 32.  Nothing else is implied: a token sees itself, or an ancestor,
+ * only where the mask says so, so any mask over the new tokens is allowed.  Bits at or past n are
+ * ignored, and so are the masks of the padding tokens t >= n (O = 0, LSE = -inf, as for a token
+ * that sees no row).
+ *   tree_mask  int32 [batch, q_len, ceil(q_len / 32)], device (mla_cache_extend writes it)
+ * A causal chain is the mask with bits 0..t set.  The new rows must be in the cache (see
+ * mla_cache_append); every row below L_b must be finite, also one that only some tokens see.  No
+ * `causal` argument; all other arguments, layouts, limits and errors as for mla_decode_fwd_ragged
+ * and mla_decode_fwd_fp8.
+ */
+MLA_API int mla_decode_fwd_tree(const void *q, const void *kv, const int32_t *seqlens, const int32_t *q_lens,
+                                const int32_t *tree_mask, const int32_t *block_table, int batch, int q_len,
+                                int num_heads, int64_t kv_rows, int max_blocks, float softmax_scale, void *o,
+                                float *lse, void *workspace, size_t workspace_bytes, int num_sms, unsigned flags,
+                                void *stream);
+MLA_API int mla_decode_fwd_tree_fp8(const void *q, const void *kv8, const float *kv_scale, const int32_t *seqlens,
+                                    const int32_t *q_lens, const int32_t *tree_mask, const int32_t *block_table,
+                                    int batch, int q_len, int num_heads, int64_t kv_rows, int max_blocks,
+                                    float softmax_scale, void *o, float *lse, void *workspace,
+                                    size_t workspace_bytes, int num_sms, unsigned flags, void *stream);
+
+/*
+ * The calls below keep the cache that the decode reads (the pages assume it filled): together with
+ * a decode they are one serving step, extend -> append -> plan + decode -> accept.  Each takes a
+ * `status` word: device int32, zeroed by the caller, that keeps the first device-side error until
+ * the caller zeroes it again (256-byte aligned, it can be read with mla_decode_read_status).
+ * Buffers must not overlap except where stated.
+ *
+ * mla_cache_extend: from the request lengths, the pages, cache rows, positions and ancestor masks
+ * of new_lens[b] (NULL: q_len) new tokens per sequence, in one kernel.
+ *   seqlens      int32 [batch], rows in the cache so far; seqlens_out, int32 [batch], receives
+ *                seqlens + new_lens (it may be seqlens itself)
+ *   block_table  int32 [batch, max_blocks], or NULL for a contiguous cache [batch, kv_rows, 576].
+ *                Entries ceil(L/64) .. ceil((L + n)/64) - 1 are written with pages taken from the
+ *                end of free_pages: int32 [free_capacity], its first *num_free entries free; the
+ *                first new page is free_pages[*num_free - 1], and so on in sequence order.
+ *                *num_free_out (it may be num_free itself) receives what is left.  The entries of
+ *                free_pages stay as they are.
+ *   kv_rows      rows of the pool (a multiple of 64), or per sequence when contiguous
+ *   slots        int32 [batch, q_len]: cache row of each new token (page * 64 + offset, or
+ *                b * kv_rows + offset); -1 for padding (t >= new_lens[b])
+ *   positions    int32 [batch, q_len]: L + t, or with parents L + the token's depth; -1 for padding
+ *   parents      int32 [batch, q_len] or NULL: the new token each new token follows (below its own
+ *                index), or -1 where it follows the context; then tree_mask, int32
+ *                [batch, q_len, ceil(q_len / 32)], receives each token's own and its ancestors' bits
+ *                (0 for padding), as mla_decode_fwd_tree reads them.  q_len <= MLA_MAX_COLUMNS.
+ * Device-side errors: new_lens outside [0, q_len] is clamped (MLA_ERR_INVALID_ARG); a parent at or
+ * past its own token, or below -1, counts as -1 (MLA_ERR_INVALID_ARG); a page outside the pool
+ * gets slot -1 for its tokens (MLA_ERR_BLOCK_TABLE).  A length below 0 or past the cache or table
+ * (MLA_ERR_INVALID_ARG), or too few free pages for the whole call (MLA_ERR_PAGES), changes
+ * nothing: lengths and page count are copied unchanged and every slot and position is -1.
+ */
+MLA_API int mla_cache_extend(const int32_t *seqlens, const int32_t *new_lens, const int32_t *parents, int batch,
+                             int q_len, int32_t *block_table, int max_blocks, const int32_t *free_pages,
+                             int free_capacity, const int32_t *num_free, int64_t kv_rows, int32_t *slots,
+                             int32_t *positions, int32_t *tree_mask, int32_t *seqlens_out, int32_t *num_free_out,
+                             int32_t *status, void *stream);
+
+/*
+ * mla_cache_append: the cache rows of new tokens, and the rotation of their queries, in one kernel.
+ * Row i of `latent` holds 512 latent and 64 rope columns; the cache row slots[i] receives
+ *     latent / sqrt(mean(latent^2) + eps) * norm_weight   (as it is, with norm_weight NULL)
+ *     rope columns rotated by the angles of positions[i]: (x cos - y sin, y cos + x sin)
+ * computed in fp32 and rounded once.  Pairs (x, y) are columns (2k, 2k + 1) with interleaved = 1,
+ * else (k, k + 32); they keep their places.
+ *   latent       bf16, `tokens` rows latent_stride elements apart (a multiple of 8, >= 576), 16-byte
+ *                aligned: it may be a slice of a wider projection
+ *   norm_weight  bf16 [512], 16-byte aligned, or NULL
+ *   rope_table   fp32 [max_pos, 64]: cosines of the 32 angles, then sines; 16-byte aligned
+ *   positions, slots  int32 [tokens] (mla_cache_extend writes them).  A token with a negative
+ *                position is padding: nothing is read or written for it.  A negative slot writes no
+ *                cache row.  A position >= max_pos (MLA_ERR_INVALID_ARG) writes nothing, a slot >=
+ *                cache_rows (MLA_ERR_BLOCK_TABLE) no cache row.  No slot may stand there twice.
+ *   kv           bf16 [cache_rows, 576], 16-byte aligned (a pool, or a contiguous cache as one)
+ *   q_rope, q    NULL, or: the queries' rope columns, bf16 [tokens, num_heads, 64] with
+ *                q_token_stride and q_head_stride elements between rows (multiples of 8), and the
+ *                decode's q, bf16 [tokens, num_heads, 576], whose columns 512..575 receive them
+ *                rotated (columns 0..511 are left as they are).  q_rope may be those very columns of q.
+ * tokens = 0 does nothing.
+ *
+ * mla_cache_append_fp8: the same into an E4M3 cache.  kv_scale[slot] receives max|row| / 448 over the
+ * row's finite values (1 for a row of zeros, and at least 2^-100), kv8 the codes of row / scale, rounded to
+ * nearest even; a value that is not finite becomes the NaN code.
+ */
+MLA_API int mla_cache_append(const void *latent, int64_t latent_stride, const void *norm_weight, float eps,
+                             const float *rope_table, int max_pos, int interleaved, const int32_t *positions,
+                             const int32_t *slots, int tokens, void *kv, int64_t cache_rows, const void *q_rope,
+                             int64_t q_token_stride, int64_t q_head_stride, int num_heads, void *q, int32_t *status,
+                             void *stream);
+MLA_API int mla_cache_append_fp8(const void *latent, int64_t latent_stride, const void *norm_weight, float eps,
+                                 const float *rope_table, int max_pos, int interleaved, const int32_t *positions,
+                                 const int32_t *slots, int tokens, void *kv8, float *kv_scale, int64_t cache_rows,
+                                 const void *q_rope, int64_t q_token_stride, int64_t q_head_stride, int num_heads,
+                                 void *q, int32_t *status, void *stream);
+
+/*
+ * mla_cache_accept: the end of a verify step.  Of sequence b's n = new_lens[b] last rows (0 <= n <=
+ * min(q_len, L)) those of the accepted path stay: row L - n + path[b][i] moves to L - n + i for
+ * i < path_lens[b], the rest is dropped.  Positions need no second rotation: a token of depth i was
+ * appended at position L - n + i.
+ *   kv, kv_scale   bf16 rows and NULL, or E4M3 codes and their row scales
+ *   path           int32 [batch, max_path]: new-token indices, rising
+ *   path_lens      int32 [batch]: 0 .. min(max_path, n), or -1: the sequence has ended (length 0)
+ *   seqlens_out    int32 [batch]: L - n + path_lens[b] (may be seqlens itself)
+ *   block_table    as for mla_cache_extend (its entries are left as they are).  Pages past the new
+ *                  length are pushed behind free_pages[*num_free - 1], in sequence order, and
+ *                  *num_free_out (may be num_free itself) receives the new count.
+ * A sequence whose lengths or path break these rules is left as it is (MLA_ERR_INVALID_ARG); a bad page
+ * leaves the rows behind it unspecified (MLA_ERR_BLOCK_TABLE); pages that do not fit free_capacity
+ * are dropped (MLA_ERR_INVALID_ARG).
+ */
+MLA_API int mla_cache_accept(void *kv, float *kv_scale, const int32_t *seqlens, const int32_t *new_lens,
+                             const int32_t *path, const int32_t *path_lens, int batch, int q_len, int max_path,
+                             const int32_t *block_table, int max_blocks, int32_t *free_pages, int free_capacity,
+                             const int32_t *num_free, int64_t kv_rows, int32_t *seqlens_out, int32_t *num_free_out,
+                             int32_t *status, void *stream);
 
 /*
  * The same decode in the untransposed form the pages set ETAP against ([TS]

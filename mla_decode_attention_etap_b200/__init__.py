@@ -24,12 +24,14 @@ FLAG_SKIP_COMBINE = 1
 FLAG_TEST_EXPIRE_WAITS = 0x40000000
 
 STATUS = {0: "MLA_OK", -1: "MLA_ERR_INVALID_ARG", -2: "MLA_ERR_UNSUPPORTED", -3: "MLA_ERR_ALIGNMENT",
-          -4: "MLA_ERR_WORKSPACE", -5: "MLA_ERR_CUDA", -6: "MLA_ERR_TIMEOUT", -7: "MLA_ERR_BLOCK_TABLE"}
+          -4: "MLA_ERR_WORKSPACE", -5: "MLA_ERR_CUDA", -6: "MLA_ERR_TIMEOUT", -7: "MLA_ERR_BLOCK_TABLE",
+          -8: "MLA_ERR_PAGES"}
 
 EXPORTS = ("mla_decode_workspace_size", "mla_decode_plan", "mla_decode_fwd", "mla_combine",
            "mla_decode_read_status", "mla_decode_plan_host", "mla_status_string", "mla_last_cuda_error",
            "mla_decode_fwd_static_ws", "mla_decode_static_ws_status", "mla_decode_fwd_ragged", "mla_stream_probe", "mla_decode_fwd_fp8", "mla_form_ablation",
-           "mla_decode_fwd_trace", "mla_decode_fwd_untransposed")
+           "mla_decode_fwd_trace", "mla_decode_fwd_untransposed", "mla_decode_fwd_tree", "mla_decode_fwd_tree_fp8",
+           "mla_cache_extend", "mla_cache_append", "mla_cache_append_fp8", "mla_cache_accept")
 STATIC_WORKSPACE_BYTES = 16777216
 
 
@@ -88,6 +90,24 @@ def lib() -> ctypes.CDLL:
         L.mla_decode_fwd_trace.restype = i32
         L.mla_stream_probe.argtypes = [vp, i64, i32, vp, vp]
         L.mla_stream_probe.restype = i32
+        f32, u32 = ctypes.c_float, ctypes.c_uint
+        L.mla_decode_fwd_tree.argtypes = [vp, vp, vp, vp, vp, vp, i32, i32, i32, i64, i32, f32, vp, vp, vp, sz, i32,
+                                          u32, vp]
+        L.mla_decode_fwd_tree.restype = i32
+        L.mla_decode_fwd_tree_fp8.argtypes = [vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i64, i32, f32, vp, vp, vp,
+                                              sz, i32, u32, vp]
+        L.mla_decode_fwd_tree_fp8.restype = i32
+        L.mla_cache_extend.argtypes = [vp, vp, vp, i32, i32, vp, i32, vp, i32, vp, i64, vp, vp, vp, vp, vp, vp, vp]
+        L.mla_cache_extend.restype = i32
+        L.mla_cache_append.argtypes = [vp, i64, vp, f32, vp, i32, i32, vp, vp, i32, vp, i64, vp, i64, i64, i32, vp,
+                                       vp, vp]
+        L.mla_cache_append.restype = i32
+        L.mla_cache_append_fp8.argtypes = [vp, i64, vp, f32, vp, i32, i32, vp, vp, i32, vp, vp, i64, vp, i64, i64,
+                                           i32, vp, vp, vp]
+        L.mla_cache_append_fp8.restype = i32
+        L.mla_cache_accept.argtypes = [vp, vp, vp, vp, vp, vp, i32, i32, i32, vp, i32, vp, i32, vp, i64, vp, vp, vp,
+                                       vp]
+        L.mla_cache_accept.restype = i32
         L.mla_last_cuda_error.argtypes = []
         L.mla_last_cuda_error.restype = ctypes.c_char_p
         _lib = L
@@ -157,6 +177,19 @@ def _require_cuda(t, name: str) -> None:
 def _stream(stream=None):
     s = stream if stream is not None else torch.cuda.current_stream()
     return ctypes.c_void_p(s.cuda_stream)
+
+
+def _launch(device, stream, call, what: str) -> None:
+    """``call(stream pointer)`` with ``device`` current, on ``stream`` or that device's current stream."""
+    if stream is not None and stream.device != device:
+        raise ValueError(f"{what}: stream on {stream.device}, tensors on {device}")
+    if device.index == torch.cuda.current_device():
+        s = stream if stream is not None else torch.cuda.current_stream(device)
+        _check(call(s.cuda_stream), what)
+    else:
+        with torch.cuda.device(device):
+            s = stream if stream is not None else torch.cuda.current_stream(device)
+            _check(call(s.cuda_stream), what)
 
 
 def num_sms(device=None) -> int:
@@ -238,6 +271,61 @@ def mla_decode_fwd_fp8(q, kv8, kv_scale, seqlens, block_table, softmax_scale, ca
                                     int(bool(causal)), _ptr(o), _ptr(lse), _ptr(workspace),
                                     workspace.numel() * workspace.element_size(), n_sms, flags, _stream(stream)),
            "mla_decode_fwd_fp8")
+
+
+def _tree_words(q_len: int) -> int:
+    return (q_len + 31) // 32
+
+
+def check_tree_args(q, kv, seqlens, block_table, tree_mask, o, lse, workspace, q_lens=None, kv_scale=None) -> None:
+    """check_decode_args, and the mask words of every query token."""
+    check_decode_args(q, kv, seqlens, block_table, o, lse, workspace, q_lens, kv_scale)
+    if block_table is not None and kv.shape[1] != PAGE_SIZE:
+        raise ValueError(f"kv: pages of {kv.shape[1]} rows, expected {PAGE_SIZE}")
+    B, q_len = q.shape[:2]
+    _require(tree_mask, "tree_mask", torch.int32, q.device)
+    if tuple(tree_mask.shape) != (B, q_len, _tree_words(q_len)):
+        raise ValueError(f"tree_mask: shape {tuple(tree_mask.shape)}, expected {(B, q_len, _tree_words(q_len))}")
+
+
+def mla_decode_fwd_tree(q, kv, seqlens, block_table, softmax_scale, tree_mask, o, lse, workspace, n_sms, flags=0,
+                        stream=None, q_lens=None) -> None:
+    """Decode of drafts that form a tree: token t sees the rows ahead of the q_lens[b] (or q_len) new
+    ones and the new tokens u whose bit is set in ``tree_mask`` (int32 [B, q_len, ceil(q_len / 32)])."""
+    _require_cuda(q, "q")
+    check_tree_args(q, kv, seqlens, block_table, tree_mask, o, lse, workspace, q_lens)
+    B, q_len, h, _ = q.shape
+    if block_table is not None:
+        kv_rows, max_blocks = kv.shape[0] * kv.shape[1], block_table.shape[1]
+    else:
+        kv_rows, max_blocks = kv.shape[1], 0
+    _launch(q.device, stream,
+            lambda s: lib().mla_decode_fwd_tree(_ptr(q), _ptr(kv), _ptr(seqlens), _ptr(q_lens), _ptr(tree_mask),
+                                                _ptr(block_table), B, q_len, h, kv_rows, max_blocks,
+                                                float(softmax_scale), _ptr(o), _ptr(lse), _ptr(workspace),
+                                                workspace.numel() * workspace.element_size(), n_sms, flags, s),
+            "mla_decode_fwd_tree")
+
+
+def mla_decode_fwd_tree_fp8(q, kv8, kv_scale, seqlens, block_table, softmax_scale, tree_mask, o, lse, workspace,
+                            n_sms, flags=0, stream=None, q_lens=None) -> None:
+    """mla_decode_fwd_tree over an FP8 cache (E4M3 codes and one fp32 scale per cache row)."""
+    _require_cuda(q, "q")
+    if kv_scale is None:
+        raise TypeError("kv_scale: expected a torch.Tensor, got NoneType")
+    check_tree_args(q, kv8, seqlens, block_table, tree_mask, o, lse, workspace, q_lens, kv_scale)
+    B, q_len, h, _ = q.shape
+    if block_table is not None:
+        kv_rows, max_blocks = kv8.shape[0] * kv8.shape[1], block_table.shape[1]
+    else:
+        kv_rows, max_blocks = kv8.shape[1], 0
+    _launch(q.device, stream,
+            lambda s: lib().mla_decode_fwd_tree_fp8(_ptr(q), _ptr(kv8), _ptr(kv_scale), _ptr(seqlens), _ptr(q_lens),
+                                                    _ptr(tree_mask), _ptr(block_table), B, q_len, h, kv_rows,
+                                                    max_blocks, float(softmax_scale), _ptr(o), _ptr(lse),
+                                                    _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                                    n_sms, flags, s),
+            "mla_decode_fwd_tree_fp8")
 
 
 TRACE_ROLES = ("K-tile producer", "step-1 issuer", "value producer", "softmax", "step-3 issuer")
@@ -333,6 +421,186 @@ def mla_combine(workspace, batch, q_len, num_heads, n_sms, o, lse, stream=None) 
            "mla_combine")
 
 
+def _int32(t, name: str, device, shape) -> int:
+    """Address of a contiguous int32 tensor of exactly this shape (None: 0), or TypeError / ValueError."""
+    if t is None:
+        return 0
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+    if t.dtype is not torch.int32:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected torch.int32")
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, expected {device} (all tensors on one device)")
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected contiguous {tuple(shape)}")
+    return t.data_ptr()
+
+
+def _status_word(status, device) -> int:
+    _require(status, "status", torch.int32, device, min_numel=1)
+    return status.data_ptr()
+
+
+def _page_stack(block_table, free_pages, num_free, num_free_out, B: int, device):
+    """Table and stack of a paged cache -> (table, max_blocks, stack, capacity, count, count out)."""
+    if block_table is None:
+        return 0, 0, 0, 0, 0, 0
+    _require(block_table, "block_table", torch.int32, device, dim=2)
+    if block_table.shape[0] != B:
+        raise ValueError(f"block_table: {block_table.shape[0]} rows, expected {B}")
+    _require(free_pages, "free_pages", torch.int32, device, dim=1)
+    return (block_table.data_ptr(), block_table.shape[1], free_pages.data_ptr(), free_pages.shape[0],
+            _int32(num_free, "num_free", device, (1,)), _int32(num_free_out, "num_free_out", device, (1,)))
+
+
+def check_extend_args(seqlens, new_lens, block_table, free_pages, num_free, slots, positions, seqlens_out,
+                      num_free_out, status, parents=None, tree_mask=None) -> list:
+    """Shapes, dtypes and devices of mla_cache_extend -> the addresses and sizes it passes on."""
+    _require(slots, "slots", torch.int32, slots.device if isinstance(slots, torch.Tensor) else None, dim=2)
+    dev, (B, q_len) = slots.device, slots.shape
+    if (parents is None) != (tree_mask is None):
+        raise ValueError("parents and tree_mask: give both or neither")
+    if block_table is not None and (num_free is None or num_free_out is None):
+        raise ValueError("num_free and num_free_out: a paged cache needs both")
+    if seqlens is None or positions is None or seqlens_out is None:
+        raise ValueError("seqlens, positions and seqlens_out are not optional")
+    table, max_blocks, stack, capacity, nfree, nfree_out = _page_stack(block_table, free_pages, num_free,
+                                                                       num_free_out, B, dev)
+    return [_int32(seqlens, "seqlens", dev, (B,)), _int32(new_lens, "new_lens", dev, (B,)),
+            _int32(parents, "parents", dev, (B, q_len)), B, q_len, table, max_blocks, stack, capacity, nfree,
+            _int32(positions, "positions", dev, (B, q_len)),
+            _int32(tree_mask, "tree_mask", dev, (B, q_len, _tree_words(q_len))),
+            _int32(seqlens_out, "seqlens_out", dev, (B,)), nfree_out, _status_word(status, dev)]
+
+
+def mla_cache_extend(seqlens, new_lens, block_table, free_pages, num_free, kv_rows: int, slots, positions,
+                     seqlens_out, num_free_out, status, parents=None, tree_mask=None, stream=None) -> None:
+    """Pages, cache rows, positions and ancestor masks of new tokens, from the request lengths.
+
+    ``slots`` and ``positions`` (int32 [B, q_len]) are written, ``block_table`` is extended with pages from
+    the end of ``free_pages``, ``seqlens_out`` and ``num_free_out`` (they may be the inputs themselves)
+    receive the new lengths and the pages left.  ``new_lens`` None: q_len for every sequence;
+    ``block_table`` None: a contiguous cache of ``kv_rows`` rows per sequence, no pages.  ``parents``
+    (int32 [B, q_len], -1 behind the context) makes the tokens a tree and fills ``tree_mask``."""
+    a = check_extend_args(seqlens, new_lens, block_table, free_pages, num_free, slots, positions, seqlens_out,
+                          num_free_out, status, parents, tree_mask)
+    _require_cuda(slots, "slots")
+    _launch(slots.device, stream,
+            lambda s: lib().mla_cache_extend(*a[:10], kv_rows, slots.data_ptr(), *a[10:], s), "mla_cache_extend")
+
+
+def check_append_args(latent, norm_weight, rope_table, positions, slots, kv, status, q_rope=None, q=None,
+                      kv_scale=None) -> tuple:
+    """Shapes, dtypes and devices of mla_cache_append(_fp8) -> (arguments ahead of the cache, the cache's,
+    those behind it)."""
+    if not isinstance(latent, torch.Tensor):
+        raise TypeError(f"latent: expected a torch.Tensor, got {type(latent).__name__}")
+    dev = latent.device
+    if latent.dtype is not torch.bfloat16:
+        raise TypeError(f"latent: dtype {latent.dtype}, expected torch.bfloat16")
+    if latent.dim() != 2 or latent.shape[1] != D_QK or (latent.shape[0] > 0 and latent.stride(1) != 1):
+        raise ValueError(f"latent: shape {tuple(latent.shape)}, expected [tokens, {D_QK}] with dense rows")
+    T = latent.shape[0]
+    if norm_weight is not None:
+        _require(norm_weight, "norm_weight", torch.bfloat16, dev, dim=1, last=D_V)
+    _require(rope_table, "rope_table", torch.float32, dev, dim=2, last=64)
+    if positions is None or slots is None:
+        raise ValueError("positions and slots are not optional")
+    fp8 = kv_scale is not None
+    _require(kv, "kv8" if fp8 else "kv", torch.uint8 if fp8 else torch.bfloat16, dev, last=D_QK)
+    rows = kv.numel() // D_QK
+    if fp8:
+        _require(kv_scale, "kv_scale", torch.float32, dev, min_numel=rows)
+    ahead = [latent.data_ptr(), max(latent.stride(0), D_QK) if T <= 1 else latent.stride(0),
+             0 if norm_weight is None else norm_weight.data_ptr()]
+    where = [_int32(positions, "positions", dev, (T,)), _int32(slots, "slots", dev, (T,)), T]
+    if (q_rope is None) != (q is None):
+        raise ValueError("q_rope and q: give both or neither")
+    queries = [0, 0, 0, 0, 0]
+    if q is not None:
+        _require(q, "q", torch.bfloat16, dev, last=D_QK)
+        if not isinstance(q_rope, torch.Tensor):
+            raise TypeError(f"q_rope: expected a torch.Tensor, got {type(q_rope).__name__}")
+        if q_rope.dtype is not torch.bfloat16:
+            raise TypeError(f"q_rope: dtype {q_rope.dtype}, expected torch.bfloat16")
+        if q_rope.device != dev:
+            raise ValueError(f"q_rope: on {q_rope.device}, expected {dev} (all tensors on one device)")
+        if q_rope.dim() != 3 or q_rope.shape[0] != T or q_rope.shape[2] != 64 or q_rope.stride(2) != 1:
+            raise ValueError(f"q_rope: shape {tuple(q_rope.shape)}, expected [{T}, heads, 64] with dense rows")
+        h = q_rope.shape[1]
+        if q.numel() != T * h * D_QK or q.dim() < 2 or q.shape[-2] != h:
+            raise ValueError(f"q: shape {tuple(q.shape)}, expected [{T}, {h}, {D_QK}] or its tokens as [B, q_len]")
+        queries = [q_rope.data_ptr(), q_rope.stride(0), q_rope.stride(1), h, q.data_ptr()]
+    cache = [kv.data_ptr(), kv_scale.data_ptr(), rows] if fp8 else [kv.data_ptr(), rows]
+    return ahead, [rope_table.data_ptr(), rope_table.shape[0]], where, cache, queries + [_status_word(status, dev)]
+
+
+def mla_cache_append(latent, norm_weight, eps, rope_table, interleaved, positions, slots, kv, status, q_rope=None,
+                     q=None, stream=None) -> None:
+    """Norm the 512 latent columns, rotate the 64 rope columns of each row of ``latent`` ([tokens, 576] bf16,
+    rows may be strided) and store the row at ``slots`` of the bf16 cache; with ``q_rope`` ([tokens, heads,
+    64], may be strided) also rotate the queries' rope columns into ``q[..., 512:]``."""
+    a = check_append_args(latent, norm_weight, rope_table, positions, slots, kv, status, q_rope, q)
+    _require_cuda(latent, "latent")
+    ahead, table, where, cache, behind = a
+    _launch(latent.device, stream,
+            lambda s: lib().mla_cache_append(*ahead, eps, *table, int(bool(interleaved)), *where, *cache, *behind, s),
+            "mla_cache_append")
+
+
+def mla_cache_append_fp8(latent, norm_weight, eps, rope_table, interleaved, positions, slots, kv8, kv_scale, status,
+                         q_rope=None, q=None, stream=None) -> None:
+    """mla_cache_append into an FP8 cache: E4M3 codes and one fp32 scale per row, max|row| / 448."""
+    if kv_scale is None:
+        raise TypeError("kv_scale: expected a torch.Tensor, got NoneType")
+    a = check_append_args(latent, norm_weight, rope_table, positions, slots, kv8, status, q_rope, q, kv_scale)
+    _require_cuda(latent, "latent")
+    ahead, table, where, cache, behind = a
+    _launch(latent.device, stream,
+            lambda s: lib().mla_cache_append_fp8(*ahead, eps, *table, int(bool(interleaved)), *where, *cache, *behind,
+                                                 s),
+            "mla_cache_append_fp8")
+
+
+def check_accept_args(kv, seqlens, new_lens, path, path_lens, block_table, free_pages, num_free, seqlens_out,
+                      num_free_out, status, kv_scale=None) -> tuple:
+    """Shapes, dtypes and devices of mla_cache_accept -> (arguments ahead of kv_rows, kv_rows, those behind)."""
+    _require(path, "path", torch.int32, path.device if isinstance(path, torch.Tensor) else None, dim=2)
+    dev, (B, P) = path.device, path.shape
+    fp8 = kv_scale is not None
+    _require(kv, "kv8" if fp8 else "kv", torch.uint8 if fp8 else torch.bfloat16, dev, dim=3, last=D_QK)
+    if fp8:
+        _require(kv_scale, "kv_scale", torch.float32, dev, min_numel=kv.shape[0] * kv.shape[1])
+    if block_table is not None:
+        if kv.shape[1] != PAGE_SIZE:
+            raise ValueError(f"kv: pages of {kv.shape[1]} rows, expected {PAGE_SIZE}")
+        if num_free is None or num_free_out is None:
+            raise ValueError("num_free and num_free_out: a paged cache needs both")
+    elif kv.shape[0] < B:
+        raise ValueError(f"kv: {kv.shape[0]} sequences, needs at least {B}")
+    if seqlens is None or new_lens is None or path_lens is None or seqlens_out is None:
+        raise ValueError("seqlens, new_lens, path_lens and seqlens_out are not optional")
+    table, max_blocks, stack, capacity, nfree, nfree_out = _page_stack(block_table, free_pages, num_free,
+                                                                       num_free_out, B, dev)
+    kv_rows = kv.shape[0] * kv.shape[1] if block_table is not None else kv.shape[1]
+    ahead = [kv.data_ptr(), kv_scale.data_ptr() if fp8 else 0, _int32(seqlens, "seqlens", dev, (B,)),
+             _int32(new_lens, "new_lens", dev, (B,)), path.data_ptr(), _int32(path_lens, "path_lens", dev, (B,)), B,
+             2 ** 31 - 1, P, table, max_blocks, stack, capacity, nfree]
+    return ahead, kv_rows, [_int32(seqlens_out, "seqlens_out", dev, (B,)), nfree_out, _status_word(status, dev)]
+
+
+def mla_cache_accept(kv, seqlens, new_lens, path, path_lens, block_table, free_pages, num_free, seqlens_out,
+                     num_free_out, status, kv_scale=None, stream=None) -> None:
+    """Keep the accepted path of each sequence's new_lens[b] last rows: row path[b, i] of them becomes row i
+    (i < path_lens[b]; -1: the sequence has ended), the rest is dropped and the pages past the new length
+    are pushed on ``free_pages``.  ``seqlens_out`` and ``num_free_out`` may be the inputs themselves;
+    ``kv_scale`` given: the FP8 cache."""
+    ahead, kv_rows, behind = check_accept_args(kv, seqlens, new_lens, path, path_lens, block_table, free_pages,
+                                               num_free, seqlens_out, num_free_out, status, kv_scale)
+    _require_cuda(kv, "kv")
+    _launch(kv.device, stream, lambda s: lib().mla_cache_accept(*ahead, kv_rows, *behind, s), "mla_cache_accept")
+
+
 def mla_decode_read_status(workspace, stream=None) -> int:
     _require_cuda(workspace, "workspace")
     out = ctypes.c_int(0)
@@ -395,6 +663,32 @@ class MlaDecoder:
         scale = softmax_scale if softmax_scale is not None else 1.0 / math.sqrt(D_QK)
         mla_decode_fwd_fp8(q, kv8, kv_scale, seqlens, block_table, scale, causal, o, lse, self.workspace, self.n_sms,
                            flags, stream, q_lens=q_lens)
+        return o, lse
+
+    def fwd_tree(self, q, kv, seqlens, tree_mask, block_table=None, softmax_scale=None, o=None, lse=None, flags=0,
+                 stream=None, q_lens=None):
+        """fwd for drafts that form a tree (mask words from mla_cache_extend, or the caller's own)."""
+        B, q_len, h, _ = q.shape
+        if o is None:
+            o = torch.empty(B, q_len, h, D_V, dtype=torch.bfloat16, device=q.device)
+        if lse is None:
+            lse = torch.empty(B, q_len, h, dtype=torch.float32, device=q.device)
+        scale = softmax_scale if softmax_scale is not None else 1.0 / math.sqrt(D_QK)
+        mla_decode_fwd_tree(q, kv, seqlens, block_table, scale, tree_mask, o, lse, self.workspace, self.n_sms, flags,
+                            stream, q_lens=q_lens)
+        return o, lse
+
+    def fwd_tree_fp8(self, q, kv8, kv_scale, seqlens, tree_mask, block_table=None, softmax_scale=None, o=None,
+                     lse=None, flags=0, stream=None, q_lens=None):
+        """fwd_tree over an FP8 cache (E4M3 codes + one fp32 scale per cache row)."""
+        B, q_len, h, _ = q.shape
+        if o is None:
+            o = torch.empty(B, q_len, h, D_V, dtype=torch.bfloat16, device=q.device)
+        if lse is None:
+            lse = torch.empty(B, q_len, h, dtype=torch.float32, device=q.device)
+        scale = softmax_scale if softmax_scale is not None else 1.0 / math.sqrt(D_QK)
+        mla_decode_fwd_tree_fp8(q, kv8, kv_scale, seqlens, block_table, scale, tree_mask, o, lse, self.workspace,
+                                self.n_sms, flags, stream, q_lens=q_lens)
         return o, lse
 
     def status(self, stream=None) -> int:

@@ -46,6 +46,8 @@ struct DecodeParams {
     const int32_t *seqlens;
     const int32_t *q_lens;  // ragged batch: query tokens per sequence (<= q_len), or NULL
     const int32_t *block_table;
+    const int32_t *tree_mask;  // tree decode: [B, q_len, tree_words] bits, see tree_sees
+    int tree_words;
     int32_t *ws;  // workspace (int32 view)
     float *opart;
     float *lsepart;
@@ -162,6 +164,29 @@ __device__ __forceinline__ float fast_exp2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// Tree decode: which of `width` (<= 64) consecutive query columns, the first of them c0, see cache row
+// rg of sequence b (bit n: column c0 + n).  The qlen real tokens are the last qlen cache rows; token t
+// sees every row ahead of them and, of the new rows L - qlen + u, those whose bit u is set in its mask.
+// Reads one word per token, and only for the new rows: a tile or two at the end of a sequence.
+__device__ __forceinline__ uint64_t tree_sees(const DecodeParams &p, int b, int L, int qlen, int rg, int c0,
+                                              int width) {
+    const int valid = min(qlen * p.num_heads - c0, width);
+    if (rg >= L || valid <= 0) return 0ull;
+    auto below = [](int n) -> uint64_t { return n >= 64 ? ~0ull : (1ull << n) - 1; };
+    const int u = rg - (L - qlen);
+    if (u < 0) return below(valid);
+    uint64_t bits = 0ull;
+    const int t_end = (c0 + valid - 1) / p.num_heads;
+    for (int t = c0 / p.num_heads; t <= t_end; ++t) {
+        const uint32_t w = (uint32_t)__ldg(p.tree_mask + ((int64_t)b * p.q_len + t) * p.tree_words + (u >> 5));
+        if ((w >> (u & 31)) & 1u) {
+            const int lo = max(t * p.num_heads - c0, 0), hi = min((t + 1) * p.num_heads - c0, valid);
+            bits |= below(hi) & ~below(lo);
+        }
+    }
+    return bits;
 }
 
 // Walks the (sequence, tile range) segments of flattened tiles [fb, fe).

@@ -131,7 +131,7 @@ enum : int {
     kEvEpiO = 40        // epilogue: outputs (or partials) stored
 };
 
-template <class C, bool TR>
+template <class C, bool TR, bool TREE>
 __device__ __forceinline__ void duo_body(const DuoMaps &tm, const DecodeParams &p, uint8_t *smem, uint32_t sbase,
                                          uint32_t tmem, uint32_t rank, int unit, int grp, int groups, bool has_work,
                                          volatile WaitCtl *wc, int32_t *status, bool &pv_pending) {
@@ -555,11 +555,16 @@ __device__ __forceinline__ void duo_body(const DuoMaps &tm, const DecodeParams &
         if (tid != 0) tr.row = nullptr;
         // Scores of 32 columns of this thread's row (block cc of its half), scaled to log2 units
         // and masked; one TMEM round trip.
+        uint32_t seen[NH / 32] = {};  // TREE: bit n of word cc: column 32 cc + n of this half sees this thread's row
         auto load_scores = [&](int cc, bool full, int rg, float (&x)[32]) {
             tmem_ld32_wait(tmem + lane_addr + C::S_COL + (uint32_t)(k & 1) * NC + half * NH + 32 * cc, x);
             if (full) {
 #pragma unroll
                 for (int n = 0; n < 32; ++n) x[n] *= p.scale_log2;
+            } else if constexpr (TREE) {
+                const uint32_t bits = cc == 0 ? seen[0] : seen[NH / 32 - 1];
+#pragma unroll
+                for (int n = 0; n < 32; ++n) x[n] = (bits >> n) & 1u ? x[n] * p.scale_log2 : -INFINITY;
             } else {
                 const int4 *v4 = reinterpret_cast<const int4 *>(vis_s + half * NH + 32 * cc);
 #pragma unroll
@@ -661,9 +666,20 @@ __device__ __forceinline__ void duo_body(const DuoMaps &tm, const DecodeParams &
                     tr.put(kEvSmS, k);
                     const int rg = tp * kDuoRows + kTileRows * (int)rank + row;
                     // every row of this CTA's tile visible to every column: no per-column mask
-                    const bool full =
-                        qlen_b == p.q_len && tp * kDuoRows + kTileRows * ((int)rank + 1) <= (p.causal ? L - qlen_b + 1 : L) &&
-                        grp * NC + NC <= p.ncols;
+                    bool full;
+                    if constexpr (TREE) {
+                        full = tp * kDuoRows + kTileRows * ((int)rank + 1) <= L - qlen_b &&
+                               grp * NC + NC <= qlen_b * p.num_heads;
+                        if (!full) {
+                            const uint64_t s = tree_sees(p, b, L, qlen_b, rg, grp * NC + half * NH, NH);
+                            seen[0] = (uint32_t)s;
+                            if constexpr (NH > 32) seen[1] = (uint32_t)(s >> 32);
+                        }
+                    } else {
+                        full = qlen_b == p.q_len &&
+                               tp * kDuoRows + kTileRows * ((int)rank + 1) <= (p.causal ? L - qlen_b + 1 : L) &&
+                               grp * NC + NC <= p.ncols;
+                    }
                     // ---- pass 1: does any score exceed its column's running maximum by > 2^THRESH?
                     bool need = first || !ok;
                     // rolled: one copy of the score read and test (instruction cache; measured faster)
@@ -880,7 +896,9 @@ __device__ __forceinline__ void duo_body(const DuoMaps &tm, const DecodeParams &
     }
 }
 
-template <class C64, class C128, bool TR = false>
+// TREE: the new rows' visibility comes from per-token ancestor masks (tree_sees) instead of a length
+// per column.
+template <class C64, class C128, bool TR = false, bool TREE = false>
 __global__ void __launch_bounds__(kDuoThreads, 1)
     etap_duo_kernel(const __grid_constant__ DuoMaps tm, const __grid_constant__ DecodeParams p) {
     using BR = DuoBars;
@@ -962,9 +980,9 @@ __global__ void __launch_bounds__(kDuoThreads, 1)
     bool pv_pending = false;
     if (span && threadIdx.x == 0) span[1] = global_timer_ns();
     if (mode == 1)
-        duo_body<C128, TR>(tm, p, smem, sbase, tmem, rank, unit, grp, groups, has_work, wc, status, pv_pending);
+        duo_body<C128, TR, TREE>(tm, p, smem, sbase, tmem, rank, unit, grp, groups, has_work, wc, status, pv_pending);
     else
-        duo_body<C64, TR>(tm, p, smem, sbase, tmem, rank, unit, grp, groups, has_work, wc, status, pv_pending);
+        duo_body<C64, TR, TREE>(tm, p, smem, sbase, tmem, rank, unit, grp, groups, has_work, wc, status, pv_pending);
     if (pv_pending) {
         // every MMA issued completes before TMEM is released (one barrier per issuing thread)
         const int fin = warp == 1 ? BR::FINAL : BR::FINAL3;

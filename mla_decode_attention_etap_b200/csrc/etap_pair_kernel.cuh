@@ -186,7 +186,9 @@ __device__ __forceinline__ uint32_t swz_off(uint32_t r, uint32_t j, uint32_t pit
     return off + ((j ^ ((off >> 7) & mask)) << 4);
 }
 
-template <class C, bool TR = false>
+// TREE: the new rows' visibility comes from per-token ancestor masks (tree_sees) instead of a length
+// per column.
+template <class C, bool TR = false, bool TREE = false>
 __global__ void __launch_bounds__(320, 1)
     etap_pair_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kv,
                      const __grid_constant__ CUtensorMap tm_qr, const __grid_constant__ CUtensorMap tm_kvr,
@@ -822,8 +824,26 @@ __global__ void __launch_bounds__(320, 1)
                         for (int n = 0; n < NH; ++n) rsq[n] = p.scale_log2;
                     }
                     // every row of the tile visible to every column: no per-column mask needed
-                    const bool full_tile =
-                        qlen_b == p.q_len && (t + 1) * kTileRows <= (p.causal ? L - qlen_b + 1 : L);
+                    bool full_tile;
+                    uint32_t seen[C::CH];  // TREE: bit n: column 16 ch + 8 half + n sees this thread's row
+                    if constexpr (TREE) {
+                        full_tile = min(grp * NG + NG, p.ncols) <= qlen_b * p.num_heads &&
+                                    (t + 1) * kTileRows <= L - qlen_b;
+#pragma unroll
+                        for (int ch = 0; ch < C::CH; ++ch)
+                            seen[ch] = full_tile ? 0u
+                                                 : (uint32_t)tree_sees(p, b, L, qlen_b, rg,
+                                                                       grp * NG + 16 * ch + 8 * half, 8);
+                    } else {
+                        full_tile = qlen_b == p.q_len && (t + 1) * kTileRows <= (p.causal ? L - qlen_b + 1 : L);
+                    }
+                    // does column 16 ch + 8 half + n see this thread's row (tiles that are not full)?
+                    auto sees = [&](int ch, int n) -> bool {
+                        if constexpr (TREE)
+                            return (seen[ch] >> n) & 1u;
+                        else
+                            return rg < __shfl_sync(0xffffffffu, vis_lane, 8 * ch + n);
+                    };
                     bool waited_prev = false, rescale_any = false, sent_next = false;
                     float xc[C::CH][8];  // CH > 1: full scores of this thread's columns, in registers
                     if constexpr (C::KV8) {
@@ -927,8 +947,7 @@ __global__ void __launch_bounds__(320, 1)
                             } else {
 #pragma unroll
                                 for (int n = 0; n < 8; ++n) {
-                                    const int vis = __shfl_sync(0xffffffffu, vis_lane, 8 * ch + n);
-                                    x[n] = (rg < vis) ? fmaf(x[n], rsq[8 * ch + n], lgs) : -INFINITY;
+                                    x[n] = sees(ch, n) ? fmaf(x[n], rsq[8 * ch + n], lgs) : -INFINITY;
                                 }
                             }
                         } else if (full_tile) {
@@ -937,8 +956,7 @@ __global__ void __launch_bounds__(320, 1)
                         } else {
 #pragma unroll
                             for (int n = 0; n < 8; ++n) {
-                                const int vis = __shfl_sync(0xffffffffu, vis_lane, 8 * ch + n);
-                                x[n] = (rg < vis) ? x[n] * p.scale_log2 : -INFINITY;
+                                x[n] = sees(ch, n) ? x[n] * p.scale_log2 : -INFINITY;
                             }
                         }
                         // running maximum: kept unless some row of the tile exceeds it by > 2^THRESH

@@ -14,6 +14,7 @@
 #include <vector>
 
 #include "mla_decode.h"
+#include "api_common.h"
 #include "etap_pair_kernel.cuh"
 #include "etap_duo_kernel.cuh"
 #include "plan_combine_kernels.cuh"
@@ -31,6 +32,12 @@ int cuda_fail(cudaError_t e, const char *what) {
     g_last_cuda_error = std::string(what) + ": " + cudaGetErrorString(e);
     return MLA_ERR_CUDA;
 }
+
+}  // namespace
+
+int mla::record_cuda_error(cudaError_t e, const char *what) { return cuda_fail(e, what); }
+
+namespace {
 
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
@@ -118,6 +125,18 @@ int ensure_smem_attr() {
         e = cudaFuncSetAttribute(mla::untransposed_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)mla::kUtSmemAlloc);
         if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
+        e = cudaFuncSetAttribute(mla::etap_pair_kernel<mla::PairCfg16, false, true>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, (int)mla::PairCfg16::SMEM_ALLOC);
+        if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
+        e = cudaFuncSetAttribute(mla::etap_pair_kernel<mla::PairCfg16E4, false, true>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, (int)mla::PairCfg16E4::SMEM_ALLOC);
+        if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
+        e = cudaFuncSetAttribute(mla::etap_pair_kernel<mla::PairCfg32E4, false, true>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, (int)mla::PairCfg32E4::SMEM_ALLOC);
+        if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
+        e = cudaFuncSetAttribute(mla::etap_duo_kernel<mla::DuoCfg64, mla::DuoCfg128, false, true>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, (int)mla::kDuoSmemAlloc);
+        if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
         done[dev] = true;
     }
     return MLA_OK;
@@ -147,6 +166,8 @@ cudaError_t launch_pair(const CUtensorMap &tm_q, const CUtensorMap &tm_kv, const
     if constexpr (!C::KV8) {
         if (p.trace) return cudaLaunchKernelEx(&cfg, mla::etap_pair_kernel<C, true>, tm_q, tm_kv, tm_qr, tm_kvr, p);
     }
+    if (p.tree_mask)
+        return cudaLaunchKernelEx(&cfg, mla::etap_pair_kernel<C, false, true>, tm_q, tm_kv, tm_qr, tm_kvr, p);
     return cudaLaunchKernelEx(&cfg, mla::etap_pair_kernel<C>, tm_q, tm_kv, tm_qr, tm_kvr, p);
 }
 
@@ -168,6 +189,8 @@ cudaError_t launch_duo(const mla::DuoMaps &maps, const mla::DecodeParams &p, int
     cfg.attrs = attr;
     cfg.numAttrs = 2;
     if (p.trace) return cudaLaunchKernelEx(&cfg, mla::etap_duo_kernel<mla::DuoCfg64, mla::DuoCfg128, true>, maps, p);
+    if (p.tree_mask)
+        return cudaLaunchKernelEx(&cfg, mla::etap_duo_kernel<mla::DuoCfg64, mla::DuoCfg128, false, true>, maps, p);
     return cudaLaunchKernelEx(&cfg, mla::etap_duo_kernel<mla::DuoCfg64, mla::DuoCfg128>, maps, p);
 }
 
@@ -213,6 +236,7 @@ const char *mla_status_string(int status) {
         case MLA_ERR_CUDA: return "MLA_ERR_CUDA";
         case MLA_ERR_TIMEOUT: return "MLA_ERR_TIMEOUT";
         case MLA_ERR_BLOCK_TABLE: return "MLA_ERR_BLOCK_TABLE";
+        case MLA_ERR_PAGES: return "MLA_ERR_PAGES";
         default: return "MLA_ERR_UNKNOWN";
     }
 }
@@ -349,7 +373,8 @@ int decode_fwd_impl(const void *q, const void *kv, const float *kv_scale, const 
                     const int32_t *q_lens, const int32_t *block_table, int batch, int q_len, int num_heads,
                     int64_t kv_rows, int max_blocks, float softmax_scale, int causal, void *o, float *lse,
                     void *workspace, size_t workspace_bytes, int num_sms, unsigned flags, void *stream,
-                    unsigned long long *trace = nullptr, int trace_cap = 0, bool untransposed = false) {
+                    unsigned long long *trace = nullptr, int trace_cap = 0, bool untransposed = false,
+                    const int32_t *tree_mask = nullptr) {
     const bool fp8 = kv_scale != nullptr;
     if (untransposed && (fp8 || q_lens || trace)) return MLA_ERR_UNSUPPORTED;
     int st = check_shape(batch, q_len, num_heads, num_sms);
@@ -368,7 +393,7 @@ int decode_fwd_impl(const void *q, const void *kv, const float *kv_scale, const 
         if ((int64_t)batch * kv_rows > INT32_MAX) return MLA_ERR_UNSUPPORTED;
     }
     if (!aligned(q, 16) || !aligned(kv, 16) || !aligned(o, 16) || !aligned(lse, 4) || !aligned(seqlens, 4) ||
-        !aligned(workspace, 256) || !aligned(q_lens, 4) || !aligned(kv_scale, 4))
+        !aligned(workspace, 256) || !aligned(q_lens, 4) || !aligned(kv_scale, 4) || !aligned(tree_mask, 4))
         return MLA_ERR_ALIGNMENT;
     const mla::WsLayout lay = mla::ws_layout(batch, q_len, num_heads, num_sms);
     if (workspace_bytes < lay.total) return MLA_ERR_WORKSPACE;
@@ -409,6 +434,8 @@ int decode_fwd_impl(const void *q, const void *kv, const float *kv_scale, const 
     p.seqlens = seqlens;
     p.q_lens = q_lens;
     p.block_table = block_table;
+    p.tree_mask = tree_mask;
+    p.tree_words = (q_len + 31) / 32;
     p.ws = reinterpret_cast<int32_t *>(ws);
     p.opart = reinterpret_cast<float *>(ws + lay.opart);
     p.lsepart = reinterpret_cast<float *>(ws + lay.lsepart);
@@ -554,6 +581,27 @@ int mla_decode_fwd_fp8(const void *q, const void *kv8, const float *kv_scale, co
     return decode_fwd_impl(q, kv8, kv_scale, seqlens, q_lens, block_table, batch, q_len, num_heads, kv_rows,
                            max_blocks, softmax_scale, causal, o, lse, workspace, workspace_bytes, num_sms, flags,
                            stream);
+}
+
+int mla_decode_fwd_tree(const void *q, const void *kv, const int32_t *seqlens, const int32_t *q_lens,
+                        const int32_t *tree_mask, const int32_t *block_table, int batch, int q_len, int num_heads,
+                        int64_t kv_rows, int max_blocks, float softmax_scale, void *o, float *lse, void *workspace,
+                        size_t workspace_bytes, int num_sms, unsigned flags, void *stream) {
+    if (!tree_mask) return MLA_ERR_INVALID_ARG;
+    return decode_fwd_impl(q, kv, nullptr, seqlens, q_lens, block_table, batch, q_len, num_heads, kv_rows, max_blocks,
+                           softmax_scale, 0, o, lse, workspace, workspace_bytes, num_sms, flags, stream, nullptr, 0,
+                           false, tree_mask);
+}
+
+int mla_decode_fwd_tree_fp8(const void *q, const void *kv8, const float *kv_scale, const int32_t *seqlens,
+                            const int32_t *q_lens, const int32_t *tree_mask, const int32_t *block_table, int batch,
+                            int q_len, int num_heads, int64_t kv_rows, int max_blocks, float softmax_scale, void *o,
+                            float *lse, void *workspace, size_t workspace_bytes, int num_sms, unsigned flags,
+                            void *stream) {
+    if (!kv_scale || !tree_mask) return MLA_ERR_INVALID_ARG;
+    return decode_fwd_impl(q, kv8, kv_scale, seqlens, q_lens, block_table, batch, q_len, num_heads, kv_rows,
+                           max_blocks, softmax_scale, 0, o, lse, workspace, workspace_bytes, num_sms, flags, stream,
+                           nullptr, 0, false, tree_mask);
 }
 
 int mla_decode_fwd_trace(const void *q, const void *kv, const int32_t *seqlens, const int32_t *block_table, int batch,
