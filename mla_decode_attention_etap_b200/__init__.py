@@ -175,21 +175,31 @@ def _require_cuda(t, name: str) -> None:
 
 
 def _stream(stream=None):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is None:
+        return ctypes.c_void_p(_raw_stream(torch._C._cuda_getDevice()))
+    return ctypes.c_void_p(stream.cuda_stream)
+
+
+def _raw_stream(index: int) -> int:
+    """The device's current stream as an address, without building a Stream object (2 us a call)."""
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
 def _launch(device, stream, call, what: str) -> None:
     """``call(stream pointer)`` with ``device`` current, on ``stream`` or that device's current stream."""
-    if stream is not None and stream.device != device:
+    if stream is None:
+        s = _raw_stream(device.index)
+    elif stream.device != device:
         raise ValueError(f"{what}: stream on {stream.device}, tensors on {device}")
-    if device.index == torch.cuda.current_device():
-        s = stream if stream is not None else torch.cuda.current_stream(device)
-        _check(call(s.cuda_stream), what)
+    else:
+        s = stream.cuda_stream
+    if device.index == torch._C._cuda_getDevice():
+        code = call(s)
     else:
         with torch.cuda.device(device):
-            s = stream if stream is not None else torch.cuda.current_stream(device)
-            _check(call(s.cuda_stream), what)
+            code = call(s)
+    if code != 0:
+        _check(code, what)
 
 
 def num_sms(device=None) -> int:
@@ -425,6 +435,11 @@ def _int32(t, name: str, device, shape) -> int:
     """Address of a contiguous int32 tensor of exactly this shape (None: 0), or TypeError / ValueError."""
     if t is None:
         return 0
+    try:
+        if t.dtype is torch.int32 and t.shape == shape and t.device == device and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
     if t.dtype is not torch.int32:
@@ -437,6 +452,11 @@ def _int32(t, name: str, device, shape) -> int:
 
 
 def _status_word(status, device) -> int:
+    try:
+        if status.dtype is torch.int32 and status.device == device and status.is_contiguous() and status.numel():
+            return status.data_ptr()
+    except AttributeError:
+        pass
     _require(status, "status", torch.int32, device, min_numel=1)
     return status.data_ptr()
 

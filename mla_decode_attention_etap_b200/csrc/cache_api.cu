@@ -32,6 +32,10 @@ int check_cache(const int32_t *block_table, int batch, int64_t kv_rows, int max_
 
 // Tokens per CTA of the extend kernel's cluster before the next CTA is added.
 constexpr int64_t kExtendTokensPerCta = 4096;
+// More tokens than the largest cluster has threads: four a thread instead of one.
+constexpr int64_t kExtendManyTokens = 8 * mla::kCacheThreads;
+// Warps that the largest accept cluster (8 CTAs, one of them for the pages) has for rows.
+constexpr int kAcceptClusterWarps = 7 * mla::kCacheThreads / 32;
 
 int append(const void *latent, int64_t latent_stride, const void *norm_weight, float eps, const float *rope_table,
            int max_pos, int interleaved, const int32_t *positions, const int32_t *slots, int tokens, void *kv,
@@ -127,6 +131,7 @@ int mla_cache_extend(const int32_t *seqlens, const int32_t *new_lens, const int3
     p.max_blocks = max_blocks;
     p.free_capacity = free_capacity;
     p.tree_words = (q_len + 31) / 32;
+    p.vector_out = q_len % 4 == 0 && is_aligned(slots, 16) && is_aligned(positions, 16);
     int ctas = 1;
     while (ctas < 8 && (int64_t)batch * q_len > ctas * kExtendTokensPerCta) ctas *= 2;
     cudaLaunchConfig_t cfg = {};
@@ -140,7 +145,9 @@ int mla_cache_extend(const int32_t *seqlens, const int32_t *new_lens, const int3
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return launched(cudaLaunchKernelEx(&cfg, mla::extend_kernel, p), "extend_kernel launch");
+    const bool many = (int64_t)batch * q_len > kExtendManyTokens;
+    return launched(cudaLaunchKernelEx(&cfg, many ? mla::extend_kernel<4> : mla::extend_kernel<1>, p),
+                    "extend_kernel launch");
 }
 
 int mla_cache_append(const void *latent, int64_t latent_stride, const void *norm_weight, float eps,
@@ -200,21 +207,35 @@ int mla_cache_accept(void *kv, float *kv_scale, const int32_t *seqlens, const in
     p.max_blocks = max_blocks;
     p.free_capacity = free_capacity;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (kv_scale)
-        mla::accept_rows_kernel<true><<<batch, mla::kAcceptThreads, 0, s>>>(p);
-    else
-        mla::accept_rows_kernel<false><<<batch, mla::kAcceptThreads, 0, s>>>(p);
-    const int rc = launched(cudaSuccess, "accept_rows_kernel launch");
-    if (rc != MLA_OK) return rc;
+    const bool fp8 = kv_scale != nullptr;
+    const int items = batch * (fp8 ? mla::kAcceptSlices<true> : mla::kAcceptSlices<false>);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(1, 1, 1);
     cfg.blockDim = dim3(mla::kCacheThreads, 1, 1);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
+    if (items <= kAcceptClusterWarps) {
+        int ctas = 2;
+        while ((ctas - 1) * (mla::kCacheThreads / 32) < items) ctas *= 2;
+        cfg.gridDim = dim3(ctas, 1, 1);
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = ctas;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        return launched(cudaLaunchKernelEx(&cfg, fp8 ? mla::accept_kernel<true> : mla::accept_kernel<false>, p),
+                        "accept_kernel launch");
+    }
+    const unsigned blocks = (items + mla::kAcceptThreads / 32 - 1) / (mla::kAcceptThreads / 32);
+    if (fp8)
+        mla::accept_rows_kernel<true><<<blocks, mla::kAcceptThreads, 0, s>>>(p);
+    else
+        mla::accept_rows_kernel<false><<<blocks, mla::kAcceptThreads, 0, s>>>(p);
+    const int rc = launched(cudaSuccess, "accept_rows_kernel launch");
+    if (rc != MLA_OK) return rc;
+    cfg.gridDim = dim3(1, 1, 1);
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
     return launched(cudaLaunchKernelEx(&cfg, mla::accept_pages_kernel, p), "accept_pages_kernel launch");
 }
 

@@ -1,12 +1,11 @@
 // The steps around the decode that keep its latent cache: pages, slots and masks of new tokens
-// (extend_kernel), their rows (append_kernel, rotate_queries), and the accepted path of a verified tree
-// (accept_rows_kernel, accept_pages_kernel).  No kernel here waits on another CTA except through the
+// (extend_kernel), their rows and rotated queries (append_kernel), and the accepted path of a verified tree
+// (accept_kernel; accept_rows_kernel with accept_pages_kernel).  No kernel here waits on another CTA except through the
 // hardware cluster barrier; every index read from memory is checked before it is used.
 #pragma once
 
 #include <cuda_bf16.h>
 #include <cstdint>
-#include <type_traits>
 
 #include "block_scan.cuh"
 #include "etap_common.cuh"
@@ -29,12 +28,17 @@ struct ExtendParams {
     int32_t *slots, *positions, *tree_mask, *seqlens_out, *num_free_out, *status;
     int64_t kv_rows;
     int batch, q_len, max_blocks, free_capacity, tree_words;
+    int vector_out;  // slots and positions may be stored four at a time
 };
 
 // One cluster of up to 8 CTAs.  Every CTA computes the page offsets of all sequences (a prefix sum of
 // the pages each needs), then, once all have read the lengths (the cluster barrier, so that lengths and
 // the page count may be updated in place), writes its share.  Sequences are taken kCacheThreads at a
 // time; a batch that fits one such chunk is read once, and its tokens are dealt over all CTAs.
+// A thread handles TOKENS neighbouring tokens at a time: 4 for many tokens (their lookups in flight
+// together and stored as one; 65536 tokens took 8.2 us with one each and 5.5 us with four), 1 for few
+// (64 tokens of a tree: 3.6 us against 4.9 us, the walks of a thread's tokens running one by one).
+template <int TOKENS>
 __global__ void __launch_bounds__(kCacheThreads) extend_kernel(const __grid_constant__ ExtendParams p) {
     __shared__ int64_t scan_smem[32];
     __shared__ int s_len[kCacheThreads], s_new[kCacheThreads], s_first[kCacheThreads];
@@ -56,6 +60,32 @@ __global__ void __launch_bounds__(kCacheThreads) extend_kernel(const __grid_cons
             return 0;
         }
         return paged ? pages_of((int64_t)L + n) - pages_of(L) : 0;
+    };
+    // Mask words of new token t of sequence b (t < 0, padding: none), at `at` in tree_mask; returns its
+    // depth.  The walk to the root visits falling indices, so the words are finished from the top down.
+    auto ancestors = [&](int b, int t, int64_t at) -> int {
+        int32_t *m = p.tree_mask + at;
+        int w = p.tree_words - 1, depth = -1;
+        uint32_t bits = 0;
+        for (int u = t; u >= 0;) {
+            for (; w > u >> 5; --w) {
+                m[w] = (int32_t)bits;
+                bits = 0;
+            }
+            bits |= 1u << (u & 31);
+            ++depth;
+            const int up = __ldg(p.parents + (int64_t)b * p.q_len + u);
+            if (up >= u || up < -1) {
+                raise_status(p.status, kStatusInvalid);
+                break;
+            }
+            u = up;
+        }
+        for (; w >= 0; --w) {
+            m[w] = (int32_t)bits;
+            bits = 0;
+        }
+        return depth;
     };
     const bool one_chunk = p.batch <= kCacheThreads;
     // this CTA's sequences (all of them when they fit one chunk)
@@ -116,57 +146,64 @@ __global__ void __launch_bounds__(kCacheThreads) extend_kernel(const __grid_cons
             }
         }
         if (tid < cn && (!one_chunk || rank == 0)) p.seqlens_out[c0 + tid] = s_len[tid] + (ok ? s_new[tid] : 0);
-        // slots, positions and ancestor masks, token by token
-        const uint32_t tokens = (uint32_t)cn * p.q_len;  // batch * q_len fits an int32
+        // slots, positions and ancestor masks: TOKENS tokens of one sequence a thread, whose page
+        // lookups are in flight together
+        const uint32_t per_seq = (uint32_t)(p.q_len + TOKENS - 1) / TOKENS;
+        const uint32_t items = (uint32_t)cn * per_seq;  // batch * q_len fits an int32
         const uint32_t estep = one_chunk ? ctas * kCacheThreads : kCacheThreads;
-        for (uint32_t e = one_chunk ? rank * kCacheThreads + tid : tid; e < tokens; e += estep) {
-            const int c = (int)(e / (uint32_t)p.q_len), t = (int)(e - (uint32_t)c * p.q_len);
-            const int b = c0 + c;
-            const int64_t at = (int64_t)b * p.q_len + t;
-            const bool real = t < s_new[c];
-            int depth = t;
-            if (p.tree_mask) {
-                // the walk to the root visits falling indices, so the words are finished from the top down
-                int32_t *m = p.tree_mask + at * p.tree_words;
-                int w = p.tree_words - 1;
-                uint32_t bits = 0;
-                depth = -1;
-                for (int u = real ? t : -1; u >= 0;) {
-                    for (; w > u >> 5; --w) {
-                        m[w] = (int32_t)bits;
-                        bits = 0;
-                    }
-                    bits |= 1u << (u & 31);
-                    ++depth;
-                    const int up = __ldg(p.parents + (int64_t)b * p.q_len + u);
-                    if (up >= u || up < -1) {
-                        raise_status(p.status, kStatusInvalid);
-                        break;
-                    }
-                    u = up;
-                }
-                for (; w >= 0; --w) {
-                    m[w] = (int32_t)bits;
-                    bits = 0;
-                }
-            }
-            int slot = -1, pos = -1;
-            if (real && ok) {
-                const int row = s_len[c] + t;
-                pos = s_len[c] + depth;
+        for (uint32_t e = one_chunk ? rank * kCacheThreads + tid : tid; e < items; e += estep) {
+            const int c = (int)(e / per_seq), t0 = (int)(e - (uint32_t)c * per_seq) * TOKENS;
+            const int b = c0 + c, L = s_len[c], n = s_new[c];
+            const int have = pages_of(L);
+            const int64_t at = (int64_t)b * p.q_len + t0;
+            int pos[TOKENS], page[TOKENS];
+#pragma unroll
+            for (int u = 0; u < TOKENS; ++u) {
+                const int t = t0 + u;
+                pos[u] = page[u] = -1;
+                if (t >= n || !ok) continue;
+                pos[u] = L + t;
                 if (paged) {
-                    const int have = pages_of(s_len[c]), i = row / kPage;
-                    const int page = i < have ? p.block_table[(int64_t)b * p.max_blocks + i] : taken(c, i - have);
-                    if (page < 0 || (int64_t)page * kPage >= p.kv_rows)
-                        raise_status(p.status, kStatusBlockTable);
-                    else
-                        slot = page * kPage + row % kPage;
-                } else {
-                    slot = (int)((int64_t)b * p.kv_rows + row);
+                    const int i = (L + t) / kPage;
+                    page[u] = i < have ? p.block_table[(int64_t)b * p.max_blocks + i] : taken(c, i - have);
                 }
             }
-            p.slots[at] = slot;
-            p.positions[at] = pos;
+            if (p.tree_mask) {
+#pragma unroll
+                for (int u = 0; u < TOKENS; ++u)
+                    if (t0 + u < p.q_len) {
+                        const int depth = ancestors(b, t0 + u < n ? t0 + u : -1, (at + u) * p.tree_words);
+                        if (pos[u] >= 0) pos[u] = L + depth;
+                    }
+            }
+            int slot[TOKENS];
+#pragma unroll
+            for (int u = 0; u < TOKENS; ++u) {
+                slot[u] = -1;
+                if (pos[u] < 0) continue;
+                if (!paged)
+                    slot[u] = (int)((int64_t)b * p.kv_rows + L + t0 + u);
+                else if (page[u] < 0 || (int64_t)page[u] * kPage >= p.kv_rows)
+                    raise_status(p.status, kStatusBlockTable);
+                else
+                    slot[u] = page[u] * kPage + (L + t0 + u) % kPage;
+            }
+            bool stored = false;
+            if constexpr (TOKENS == 4) {
+                if (p.vector_out) {
+                    *reinterpret_cast<int4 *>(p.slots + at) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+                    *reinterpret_cast<int4 *>(p.positions + at) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+                    stored = true;
+                }
+            }
+            if (!stored) {
+#pragma unroll
+                for (int u = 0; u < TOKENS; ++u)
+                    if (t0 + u < p.q_len) {
+                        p.slots[at + u] = slot[u];
+                        p.positions[at + u] = pos[u];
+                    }
+            }
         }
         if (!one_chunk) __syncthreads();  // the shared arrays are rewritten for the next chunk
     }
@@ -406,34 +443,43 @@ __device__ __forceinline__ AcceptSeq accept_seq(const AcceptParams &p, int b) {
               s.keep <= p.max_path && s.keep <= s.n;
     return s;
 }
-// Entry i of a path: inside the new tokens and above entry i - 1.
-__device__ __forceinline__ bool path_entry_ok(const int32_t *path, int i, int n) {
-    const int v = path[i];
-    return v < n && v > (i > 0 ? path[i - 1] : -1);
+// Lengths and path of sequence b, read together by a warp: lane i gets entry i of the path in `v`.  False
+// where the sequence has to stay as it is; the entries must rise and lie inside the new tokens.
+__device__ __forceinline__ bool accept_read(const AcceptParams &p, int b, AcceptSeq &s, int &v) {
+    const int lane = threadIdx.x & 31;
+    const int32_t *path = p.path + (int64_t)b * p.max_path;
+    v = lane < p.max_path ? path[lane] : 0;
+    s = accept_seq(p, b);
+    bool bad = !s.valid;
+    int before = -1;  // the last entry of the 32 ahead
+    for (int i0 = 0; !bad && i0 < s.keep; i0 += 32) {
+        const int i = i0 + lane;
+        const int e = i0 == 0 ? v : i < s.keep ? path[i] : 0;
+        const int up = __shfl_up_sync(0xffffffffu, e, 1);
+        bad = __any_sync(0xffffffffu, i < s.keep && (e >= s.n || e <= (lane == 0 ? before : up)));
+        before = __shfl_sync(0xffffffffu, e, 31);
+    }
+    return !bad;
 }
 
-// One CTA per sequence moves the accepted rows: row ctx + path[i] to row ctx + i.  path[i] >= i, so a
-// thread that carries one 16-byte column (or the row scale) through all rows in rising order never
-// overwrites a row that it has yet to read, and threads never meet: no barrier between rows.
-constexpr int kAcceptThreads = 96;
-constexpr int kAcceptBatch = 8;   // rows in flight per thread
-constexpr int kAcceptChunk = 512; // rows whose places are looked up at a time
+// A warp moves one slice of a sequence's accepted rows: 32 of the 16-byte columns of a row (E4M3: the last
+// slice also the row scales, in lane 4).  Row ctx + path[i] goes to row ctx + i; path[i] >= i, so a lane
+// that carries its column through the rows in rising order, kAcceptBatch read before the first of them
+// is written, never overwrites a row that it has yet to read, and lanes and warps never meet.  The
+// path's rows are looked up by the warp 32 at a time, one a lane.  `lengths_read` is called once the
+// lengths have been read.
+constexpr int kAcceptBatch = 8;
 template <bool FP8>
-__global__ void __launch_bounds__(kAcceptThreads) accept_rows_kernel(const __grid_constant__ AcceptParams p) {
-    __shared__ int s_src[kAcceptChunk], s_dst[kAcceptChunk];
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int b = blockIdx.x, tid = threadIdx.x;
-    const AcceptSeq s = accept_seq(p, b);
-    if (!s.valid) {
-        if (tid == 0) raise_status(p.status, kStatusInvalid);
-        return;
-    }
-    if (s.keep <= 0) return;
-    const int32_t *path = p.path + (int64_t)b * p.max_path;
-    bool bad = false;
-    for (int i = tid; i < s.keep; i += kAcceptThreads) bad |= !path_entry_ok(path, i, s.n);
-    if (__syncthreads_or(bad)) {
-        if (tid == 0) raise_status(p.status, kStatusInvalid);
+constexpr int kAcceptSlices = FP8 ? 2 : 3;
+template <bool FP8, class Read>
+__device__ __forceinline__ void accept_rows(const AcceptParams &p, int b, int slice, Read lengths_read) {
+    const int lane = threadIdx.x & 31;
+    AcceptSeq s;
+    int v0;
+    const bool good = accept_read(p, b, s, v0);
+    lengths_read();
+    if (!good) {
+        if (lane == 0 && slice == 0) raise_status(p.status, kStatusInvalid);
         return;
     }
     const int ctx = s.L - s.n;
@@ -447,44 +493,44 @@ __global__ void __launch_bounds__(kAcceptThreads) accept_rows_kernel(const __gri
         return page * kPage + row % kPage;
     };
     constexpr int kChunks = FP8 ? kDqk / 16 : kDqk * 2 / 16;  // 16-byte columns of a row
-    for (int c0 = 0; c0 < s.keep; c0 += kAcceptChunk) {
-        const int cn = min(s.keep - c0, kAcceptChunk);
-        if (c0 > 0) __syncthreads();
-        for (int i = tid; i < cn; i += kAcceptThreads) {
-            const int from = path[c0 + i], to = c0 + i;
-            int src = -1, dst = -1;
-            if (from != to) {
+    const int col = 32 * slice + lane;
+    const bool data = col < kChunks, scale = FP8 && col == kChunks;
+    uint4 *rows = reinterpret_cast<uint4 *>(p.kv) + col;
+    for (int i0 = 0; i0 < s.keep; i0 += 32) {
+        int src = -1, dst = -1;
+        if (i0 + lane < s.keep) {
+            const int from = i0 == 0 ? v0 : p.path[(int64_t)b * p.max_path + i0 + lane];
+            if (from != i0 + lane) {
                 src = locate(ctx + from);
-                dst = locate(ctx + to);
+                dst = locate(ctx + i0 + lane);
+                if (dst < 0) src = -1;
             }
-            s_src[i] = dst < 0 ? -1 : src;
-            s_dst[i] = dst;
         }
-        __syncthreads();
-        // kAcceptBatch rows are read before the first of them is written: their places lie below every
-        // later source
-        auto carry = [&](auto *rows, int pitch) {
-            for (int i0 = 0; i0 < cn; i0 += kAcceptBatch) {
-                std::remove_reference_t<decltype(*rows)> v[kAcceptBatch];
+        const int end = min(s.keep - i0, 32);
+        for (int j0 = 0; j0 < end; j0 += kAcceptBatch) {
+            uint4 v[kAcceptBatch];
 #pragma unroll
-                for (int u = 0; u < kAcceptBatch; ++u)
-                    if (i0 + u < cn && s_src[i0 + u] >= 0) v[u] = rows[(int64_t)s_src[i0 + u] * pitch];
-#pragma unroll
-                for (int u = 0; u < kAcceptBatch; ++u)
-                    if (i0 + u < cn && s_src[i0 + u] >= 0) rows[(int64_t)s_dst[i0 + u] * pitch] = v[u];
+            for (int u = 0; u < kAcceptBatch; ++u) {
+                const int64_t r = __shfl_sync(0xffffffffu, src, j0 + u);  // -1 past the path's end
+                if (r >= 0 && data) v[u] = rows[r * kChunks];
+                if (r >= 0 && scale) v[u].x = __float_as_uint(p.kv_scale[r]);
             }
-        };
-        if (tid < kChunks)
-            carry(reinterpret_cast<uint4 *>(p.kv) + tid, kChunks);
-        else if (FP8 && tid == kChunks)
-            carry(p.kv_scale, 1);
+#pragma unroll
+            for (int u = 0; u < kAcceptBatch; ++u) {
+                const int64_t r = __shfl_sync(0xffffffffu, src, j0 + u);
+                const int64_t w = __shfl_sync(0xffffffffu, dst, j0 + u);
+                if (r >= 0 && data) rows[w * kChunks] = v[u];
+                if (r >= 0 && scale) p.kv_scale[w] = __uint_as_float(v[u].x);
+            }
+        }
     }
 }
 
 // One CTA: the new lengths, and the pages past them pushed on the stack in sequence order.  It reads
-// nothing that the rows' kernel writes, so it runs beside it (a programmatic dependent) and waits for
-// it only before it writes, which is what makes an update in place safe.
-__global__ void __launch_bounds__(kCacheThreads) accept_pages_kernel(const __grid_constant__ AcceptParams p) {
+// nothing that accept_rows writes; `others_have_read` returns once every reader of the lengths is done,
+// and only then is anything written, so that lengths and page count may be updated in place.
+template <class Wait>
+__device__ __forceinline__ void accept_pages(const AcceptParams &p, Wait others_have_read) {
     __shared__ int64_t scan_smem[32];
     __shared__ int s_len[kCacheThreads], s_want[kCacheThreads], s_first[kCacheThreads];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -495,15 +541,12 @@ __global__ void __launch_bounds__(kCacheThreads) accept_pages_kernel(const __gri
     for (int c0 = 0; c0 < p.batch; c0 += kCacheThreads) {
         const int cn = min(p.batch - c0, kCacheThreads);
         for (int c = warp; c < cn; c += kCacheThreads / 32) {
-            const AcceptSeq s = accept_seq(p, c0 + c);
-            bool bad = !s.valid;
-            if (!bad)
-                for (int i = lane; i < s.keep; i += 32)
-                    bad |= !path_entry_ok(p.path + (int64_t)(c0 + c) * p.max_path, i, s.n);
-            bad = __any_sync(0xffffffffu, bad);
+            AcceptSeq s;
+            int v;
+            const bool good = accept_read(p, c0 + c, s, v);
             if (lane == 0) {
                 s_len[c] = s.L;
-                s_want[c] = bad ? s.L : (s.keep < 0 ? 0 : s.L - s.n + s.keep);  // a bad path keeps its rows
+                s_want[c] = !good ? s.L : (s.keep < 0 ? 0 : s.L - s.n + s.keep);  // a bad path keeps its rows
             }
         }
         __syncthreads();
@@ -513,7 +556,7 @@ __global__ void __launch_bounds__(kCacheThreads) accept_pages_kernel(const __gri
         // (an int32: more pages than that go back only where a page stands in a table twice)
         s_first[tid] = (int)(base + block_exclusive_scan(back, scan_smem, &sum));
         __syncthreads();
-        if (c0 == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+        if (c0 == 0) others_have_read();
         if (tid < cn) p.seqlens_out[c0 + tid] = s_want[tid];
         for (int c = warp; c < cn && paged; c += kCacheThreads / 32) {
             const int want = pages_of(s_want[c]), more = pages_of(s_len[c]) - want;
@@ -532,6 +575,44 @@ __global__ void __launch_bounds__(kCacheThreads) accept_pages_kernel(const __gri
         if (!stack_ok || total > p.free_capacity) raise_status(p.status, kStatusInvalid);
         *p.num_free_out = !stack_ok ? nfree : (int)(total > p.free_capacity ? p.free_capacity : total);
     }
+}
+
+// A small batch: one cluster.  CTA 0 takes lengths and pages, the warps of the others the rows; they
+// arrive on the cluster barrier as soon as they have read the lengths (all that CTA 0 waits for: the
+// values have been used by then, so the arrival needs no ordering of its own).
+template <bool FP8>
+__global__ void __launch_bounds__(kCacheThreads) accept_kernel(const __grid_constant__ AcceptParams p) {
+    auto arrive = [] { asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory"); };
+    auto wait = [] { asm volatile("barrier.cluster.wait;" ::: "memory"); };
+    if (blockIdx.x == 0) {
+        accept_pages(p, [&] {
+            arrive();
+            wait();
+        });
+        return;
+    }
+    constexpr int kSlices = kAcceptSlices<FP8>;
+    const int i = ((int)blockIdx.x - 1) * (kCacheThreads / 32) + (int)(threadIdx.x >> 5);
+    if (i < p.batch * kSlices)
+        accept_rows<FP8>(p, i / kSlices, i % kSlices, arrive);
+    else
+        arrive();
+    __syncwarp();
+    wait();
+}
+
+// A large one: a grid of warps, and beside it (a programmatic dependent, which waits for the grid's end
+// before it writes) the CTA for lengths and pages.
+constexpr int kAcceptThreads = 128;
+template <bool FP8>
+__global__ void __launch_bounds__(kAcceptThreads) accept_rows_kernel(const __grid_constant__ AcceptParams p) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    constexpr int kSlices = kAcceptSlices<FP8>;
+    const int i = (int)blockIdx.x * (kAcceptThreads / 32) + (int)(threadIdx.x >> 5);
+    if (i < p.batch * kSlices) accept_rows<FP8>(p, i / kSlices, i % kSlices, [] {});
+}
+__global__ void __launch_bounds__(kCacheThreads) accept_pages_kernel(const __grid_constant__ AcceptParams p) {
+    accept_pages(p, [] { asm volatile("griddepcontrol.wait;" ::: "memory"); });
 }
 
 }  // namespace mla
