@@ -255,7 +255,7 @@ MLA_API int mla_cache_extend(const int32_t *seqlens, const int32_t *new_lens, co
  *   norm_weight  bf16 [512], 16-byte aligned, or NULL
  *   rope_table   fp32 [max_pos, 64]: cosines of the 32 angles, then sines; 16-byte aligned
  *   positions, slots  int32 [tokens] (mla_cache_extend writes them).  A token with a negative
- *                position is padding: nothing is read or written for it.  A negative slot writes no
+ *                position is padding: nothing is written for it.  A negative slot writes no
  *                cache row.  A position >= max_pos (MLA_ERR_INVALID_ARG) writes nothing, a slot >=
  *                cache_rows (MLA_ERR_BLOCK_TABLE) no cache row.  No slot may stand there twice.
  *   kv           bf16 [cache_rows, 576], 16-byte aligned (a pool, or a contiguous cache as one)

@@ -244,9 +244,10 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
                       pack_bf16x2(x[6], x[7]));
 }
 
-// E4M3 codes of 8 values divided by the row's scale (round to nearest even, as a cache quantised on the
-// host holds them); a value that is not finite becomes the NaN code.
-__device__ __forceinline__ uint2 codes8(const float (&x)[8], float scale) {
+// E4M3 codes of 8 values divided by the row's scale, given its reciprocal (the quotient is off by 2^-23,
+// which moves a code only where it lies that near to the border of two); a value that is not finite
+// becomes the NaN code.
+__device__ __forceinline__ uint2 codes8(const float (&x)[8], float inv) {
     uint32_t w[2] = {0u, 0u};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -254,7 +255,7 @@ __device__ __forceinline__ uint2 codes8(const float (&x)[8], float scale) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const float v = x[2 * i + j];
-            y[j] = fabsf(v) < INFINITY ? v / scale : __uint_as_float(0x7FFFFFFFu);
+            y[j] = fabsf(v) < INFINITY ? v * inv : __uint_as_float(0x7FFFFFFFu);
         }
         w[i >> 1] |= (uint32_t)f32x2_to_e4m3x2(y[0], y[1]) << (16 * (i & 1));
     }
@@ -297,7 +298,7 @@ __device__ __forceinline__ void load_angles(const float *table, int pos, int i, 
 }
 
 // One launch for both parts.  Rows: a warp per token; a lane holds two 16-byte chunks of the latent (the
-// sum of squares is one warp reduction) and lanes 0..3 two chunks of the rope columns, so that the row
+// sum of squares is one warp reduction) and two of the rope columns (eight lanes alike), so that the row
 // is read once, kept in registers through norm, rotation and quantisation, and written once.  Queries:
 // four threads per head's 64 columns, each for kQueryHeads heads of one token, with the angles kept in
 // registers across them.
@@ -307,23 +308,25 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
         const int lane = threadIdx.x & 31;
         const int tok = blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5);
         if (tok >= p.tokens) return;
-        const int pos = p.positions[tok], slot = p.slots[tok];
+        // everything that does not hang on the position is in flight before the position is known
         const uint4 *src = reinterpret_cast<const uint4 *>(p.latent + (int64_t)tok * p.row_stride);
+        const int pos = p.positions[tok], slot = p.slots[tok];
+        const uint4 l0 = __ldg(src + lane), l1 = __ldg(src + 32 + lane);
+        const int i = lane & 3;
+        const uint4 k0 = __ldg(src + 64 + rope_chunk<INTERLEAVED>(i, 0));
+        const uint4 k1 = __ldg(src + 64 + rope_chunk<INTERLEAVED>(i, 1));
         if (pos < 0 || slot < 0) return;  // padding
         if (pos >= p.max_pos || slot >= p.cache_rows) {
             if (lane == 0) raise_status(p.status, pos >= p.max_pos ? kStatusInvalid : kStatusBlockTable);
             return;
         }
-        float x0[8], x1[8], ra[8], rb[8];
-        unpack8(__ldg(src + lane), x0);
-        unpack8(__ldg(src + 32 + lane), x1);
-        if (lane < 4) {
-            float c[8], s[8];
-            load_angles(p.rope_table, pos, lane, c, s);
-            unpack8(__ldg(src + 64 + rope_chunk<INTERLEAVED>(lane, 0)), ra);
-            unpack8(__ldg(src + 64 + rope_chunk<INTERLEAVED>(lane, 1)), rb);
-            rotate16<INTERLEAVED>(ra, rb, c, s);
-        }
+        float x0[8], x1[8], ra[8], rb[8], c[8], s[8];
+        load_angles(p.rope_table, pos, i, c, s);
+        unpack8(l0, x0);
+        unpack8(l1, x1);
+        unpack8(k0, ra);
+        unpack8(k1, rb);
+        rotate16<INTERLEAVED>(ra, rb, c, s);  // in every lane, of chunk pair lane % 4
         if (p.norm_weight) {
             float sum = 0.f;
 #pragma unroll
@@ -351,20 +354,19 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
             };
             widen(x0);
             widen(x1);
-            if (lane < 4) {
-                widen(ra);
-                widen(rb);
-            }
+            widen(ra);
+            widen(rb);
 #pragma unroll
             for (int d = 16; d >= 1; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
             // 1 for a row of zeros; never under 2^-100, the least scale the decode tells apart
             const float scale = amax > 0.f ? fmaxf(amax / 448.f, 0x1p-100f) : 1.f;
+            const float inv = 1.f / scale;
             uint2 *dst = reinterpret_cast<uint2 *>(p.kv8 + (int64_t)slot * kDqk);
-            dst[lane] = codes8(x0, scale);
-            dst[32 + lane] = codes8(x1, scale);
+            dst[lane] = codes8(x0, inv);
+            dst[32 + lane] = codes8(x1, inv);
             if (lane < 4) {
-                dst[64 + rope_chunk<INTERLEAVED>(lane, 0)] = codes8(ra, scale);
-                dst[64 + rope_chunk<INTERLEAVED>(lane, 1)] = codes8(rb, scale);
+                dst[64 + rope_chunk<INTERLEAVED>(lane, 0)] = codes8(ra, inv);
+                dst[64 + rope_chunk<INTERLEAVED>(lane, 1)] = codes8(rb, inv);
             }
             if (lane == 0) p.kv_scale[slot] = scale;
         } else {
