@@ -152,6 +152,31 @@ __device__ __forceinline__ bool poll_phase(uint32_t bar, uint32_t parity, volati
         }
     }
 }
+// The same for a whole converged warp (every lane polls), on a phase to which the peer CTA contributes:
+// relaxed cluster-scope probes, then the acquire fence that pairs with the peer's release.
+__device__ __forceinline__ bool poll_phase_cluster(uint32_t bar, uint32_t parity, volatile WaitCtl *wc,
+                                                   int32_t *status) {
+    bool ok = true;
+    if (!mbar_test_wait_cluster(bar, parity)) {
+        const uint64_t t0 = global_timer_ns();
+        for (uint32_t spin = 1; !mbar_test_wait_cluster(bar, parity); ++spin) {
+            if ((spin & 255u) == 0) {
+                if (wc->abort) {
+                    ok = false;
+                    break;
+                }
+                if (global_timer_ns() - t0 > wc->limit_ns) {
+                    wc->abort = 1;
+                    atomicCAS(status, 0, kStatusTimeout);
+                    ok = false;
+                    break;
+                }
+            }
+        }
+    }
+    fence_acquire_cluster_smem();
+    return ok;
+}
 // Wait used only while draining after an abort: bounded, ignores the abort flag.
 __device__ __forceinline__ void drain_phase(uint32_t bar, uint32_t parity) {
     const uint64_t t0 = global_timer_ns();

@@ -205,49 +205,62 @@ __device__ __forceinline__ void duo_body(const DuoMaps &tm, const DecodeParams &
 
     if (warp == 0) {
         // ------------------------------------------------------------ K tiles and Q (step-1 operands)
-        if (lane == 0 && fb < fe) {
-            bool ok = true;
-            TraceRowT<TR> tr;
-            tr.init(p, 0);
-            SegIter it;
-            it.init_at(seq0, fb, fe);
-            int b, t0, t1, seg = 0;
-            uint32_t g1 = 0;
-            while (ok && it.next(tile_off, b, t0, t1)) {
-                const int L = seq_len(b);
+        // The loops of warps 0, 1, 2 and 11 are run by the whole warp; one lane issues (see elect_one).
+        const bool lead = elect_one();
+        bool ok = true;
+        TraceRowT<TR> tr;
+        tr.init(p, 0);
+        if (!lead) tr.row = nullptr;
+        TileCursor w;
+        w.valid = false;
+        if (fb < fe) w.init(tile_off, seq0, fb, fe);
+        int seg = 0, y[2];
+        bool loaded[2];
+        uint32_t g1 = 0;
+        if (w.valid) locate(w.b, w.t * kDuoRows + kTileRows * (int)rank, seq_len(w.b), y, loaded);
+        while (__all_sync(0xffffffffu, ok && w.valid)) {
+            const int y0 = __shfl_sync(0xffffffffu, loaded[0] ? y[0] : -1, 0);
+            const int y1 = __shfl_sync(0xffffffffu, loaded[1] ? y[1] : -1, 0);
+            const uint32_t nload = (y0 >= 0 ? 1u : 0u) + (y1 >= 0 ? 1u : 0u);
+            if (__any_sync(0xffffffffu, w.first())) {
                 if (seg > 0) ok = poll_phase(bar(BR::QE), (seg - 1) & 1, wc, status);
+                ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
-                if (!p.withhold_q) {
+                if (!p.withhold_q && lead) {
                     expect0(BR::QF, 9 * C::Q_CHUNK);
-                    const int qrow = b * p.ncols + grp * NC + (int)rank * NH;
+                    const int qrow = w.b * p.ncols + grp * NC + (int)rank * NH;
                     for (int i = 0; i < 9; ++i)
                         tma_load_2d_pair(sbase + C::OFF_Q + i * C::Q_CHUNK, tm_q, bar0(BR::QF), 64 * i, qrow);
                     tr.put(kEvQ, seg);
                 }
-                for (int tp = t0; tp < t1 && ok; ++tp) {
-                    int y[2];
-                    bool loaded[2];
-                    locate(b, tp * kDuoRows + kTileRows * (int)rank, L, y, loaded);
-                    const int nload = (int)loaded[0] + (int)loaded[1];
-                    // rows past the end need no zeroing here: their scores are masked to -inf
-                    for (int i = 0; i < 9 && ok; ++i, ++g1) {
-                        const int s = (int)(g1 % C::NS1);
-                        ok = poll_phase(bar(BR::S1E + s), ((g1 / C::NS1) & 1) ^ 1, wc, status);
-                        if (!ok) break;
-                        expect0(BR::S1F + s, nload * C::HALF);
-                        for (int hh = 0; hh < 2; ++hh)
-                            if (loaded[hh])
-                                tma_load_2d_pair(sbase + C::OFF_S1 + s * C::CHUNK + hh * C::HALF, &tm.kv,
-                                                 bar0(BR::S1F + s), 64 * i, y[hh]);
-                        tr.put(kEvKChunk, (int)g1);
-                    }
-                }
+                __syncwarp();
                 ++seg;
             }
-            // Tail: the last releases of the slots and of Q arrive by multicast commit; wait for them
-            // so that nothing lands in this CTA's shared memory after it leaves.
+            // the next unit's rows are looked up while this one's slots come free
+            w.advance(tile_off);
+            if (w.valid) locate(w.b, w.t * kDuoRows + kTileRows * (int)rank, seq_len(w.b), y, loaded);
+            // rows past the end need no zeroing here: their scores are masked to -inf
+#pragma unroll 1
+            for (int i = 0; i < 9; ++i, ++g1) {
+                const uint32_t s = g1 % C::NS1;
+                ok = poll_phase(bar(BR::S1E + (int)s), ((g1 / C::NS1) & 1) ^ 1, wc, status);
+                if (!__all_sync(0xffffffffu, ok)) break;
+                if (lead) {
+                    expect0(BR::S1F + (int)s, nload * C::HALF);
+                    const uint32_t dst = sbase + C::OFF_S1 + s * C::CHUNK;
+                    if (y0 >= 0) tma_load_2d_pair(dst, &tm.kv, bar0(BR::S1F + (int)s), 64 * i, y0);
+                    if (y1 >= 0) tma_load_2d_pair(dst + C::HALF, &tm.kv, bar0(BR::S1F + (int)s), 64 * i, y1);
+                    tr.put(kEvKChunk, (int)g1);
+                }
+                __syncwarp();
+            }
+            ok = __all_sync(0xffffffffu, ok);
+        }
+        // Tail: the last releases of the slots and of Q arrive by multicast commit; wait for them
+        // so that nothing lands in this CTA's shared memory after it leaves.
+        if (fb < fe) {
             for (uint32_t g = g1; ok && g < g1 + C::NS1; ++g)
-                ok = poll_phase(bar(BR::S1E + g % C::NS1), ((g / C::NS1) & 1) ^ 1, wc, status);
+                ok = poll_phase(bar(BR::S1E + (int)(g % C::NS1)), ((g / C::NS1) & 1) ^ 1, wc, status);
             if (ok && seg > 0) ok = poll_phase(bar(BR::QE), (seg - 1) & 1, wc, status);
         }
         __syncwarp();
@@ -255,149 +268,155 @@ __device__ __forceinline__ void duo_body(const DuoMaps &tm, const DecodeParams &
         // ------------------------------------------------------------ value columns (step-3 operands)
         // Unit tp, K-half h (rows 256 tp + 128 h ..), M-block j: this CTA's latent columns
         // 256 rank + 128 j .. + 127 of those rows, as one 32 KB slot of two 64-column chunks.
-        if (fb < fe) {
-            bool ok = true;
-            TraceRowT<TR> tr;
-            tr.init(p, 2);
-            SegIter it;
-            it.init_at(seq0, fb, fe);
-            int b, t0, t1, tail_uses = 0;
-            uint32_t g3 = 0;
-            while (ok && it.next(tile_off, b, t0, t1)) {
-                const int L = seq_len(b);
-                for (int tp = t0; tp < t1 && ok; ++tp) {
-                    for (int v = 0; v < 4 && ok; ++v, ++g3) {
-                        const int h = v >> 1, j = v & 1;
-                        const int s = (int)(g3 % C::NS3);
-                        // lane 0 polls; the warp follows (it zeroes tails together)
-                        if (lane == 0) ok = poll_phase(bar(BR::S3E + s), ((g3 / C::NS3) & 1) ^ 1, wc, status);
-                        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-                        if (!ok) break;
-                        int y[2];
-                        bool loaded[2];
-                        const int valid = locate(b, tp * kDuoRows + kTileRows * h, L, y, loaded);
-                        const int x0 = 256 * (int)rank + 128 * j;
-                        const uint32_t dst = sbase + C::OFF_S3 + s * C::VPAIR;
-                        if (valid == kTileRows && loaded[0] && loaded[1]) {
-                            if (lane == 0) {
-                                expect0(BR::S3F + s, C::VPAIR);
-                                for (int hc = 0; hc < 2; ++hc)
-                                    for (int hh = 0; hh < 2; ++hh)
-                                        tma_load_2d_pair(dst + hc * C::CHUNK + hh * C::HALF, &tm.kv, bar0(BR::S3F + s),
-                                                         x0 + 64 * hc, y[hh]);
-                                tr.put(kEvVPair, (int)g3);
+        const bool lead = elect_one();
+        bool ok = true;
+        TraceRowT<TR> tr;
+        tr.init(p, 2);
+        if (!lead) tr.row = nullptr;
+        TileCursor w;
+        w.valid = false;
+        if (fb < fe) w.init(tile_off, seq0, fb, fe);
+        int tail_uses = 0, L = 0, t = 0, y[2][2];
+        bool loaded[2][2];
+        uint32_t g3 = 0;
+        auto look_up = [&] {  // both K-halves of the unit
+            if (!w.valid) return;
+            L = seq_len(w.b);
+            t = w.t;
+            locate(w.b, t * kDuoRows, L, y[0], loaded[0]);
+            locate(w.b, t * kDuoRows + kTileRows, L, y[1], loaded[1]);
+        };
+        look_up();
+        while (__all_sync(0xffffffffu, ok && w.valid)) {
+            int ya[2], yb[2], valid[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                ya[h] = __shfl_sync(0xffffffffu, loaded[h][0] ? y[h][0] : -1, 0);
+                yb[h] = __shfl_sync(0xffffffffu, loaded[h][1] ? y[h][1] : -1, 0);
+                valid[h] = __shfl_sync(0xffffffffu, min(max(L - t * kDuoRows - kTileRows * h, 0), kTileRows), 0);
+            }
+            w.advance(tile_off);
+            look_up();  // of the next unit, while this one's slots come free
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll 1
+                for (int j = 0; j < 2; ++j, ++g3) {
+                    const uint32_t s = g3 % C::NS3;
+                    ok = poll_phase(bar(BR::S3E + (int)s), ((g3 / C::NS3) & 1) ^ 1, wc, status);
+                    if (!__all_sync(0xffffffffu, ok)) break;
+                    const int x0 = 256 * (int)rank + 128 * j;
+                    const uint32_t dst = sbase + C::OFF_S3 + s * C::VPAIR;
+                    if (valid[h] == kTileRows && ya[h] >= 0 && yb[h] >= 0) {
+                        if (lead) {
+                            expect0(BR::S3F + (int)s, C::VPAIR);
+#pragma unroll
+                            for (int hc = 0; hc < 2; ++hc) {
+                                tma_load_2d_pair(dst + hc * C::CHUNK, &tm.kv, bar0(BR::S3F + (int)s), x0 + 64 * hc, ya[h]);
+                                tma_load_2d_pair(dst + hc * C::CHUNK + C::HALF, &tm.kv, bar0(BR::S3F + (int)s),
+                                                 x0 + 64 * hc, yb[h]);
                             }
-                        } else {
-                            // a tail: land the valid rows, zero all others, so that whatever the cache (or
-                            // the slot) holds there meets P = 0 as an exact 0
-                            const int nload = (int)loaded[0] + (int)loaded[1];
-                            if (nload > 0) {
-                                if (lane == 0) {
-                                    mbar_arrive_expect_tx(bar(BR::TAIL), 2 * nload * C::HALF);
-                                    for (int hc = 0; hc < 2; ++hc)
-                                        for (int hh = 0; hh < 2; ++hh)
-                                            if (loaded[hh])
-                                                tma_load_2d(dst + hc * C::CHUNK + hh * C::HALF, &tm.kv, bar(BR::TAIL),
-                                                            x0 + 64 * hc, y[hh]);
-                                }
-                                if (lane == 0) ok = wait_phase(bar(BR::TAIL), tail_uses & 1, wc, status);
-                                ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-                                ++tail_uses;
-                                if (!ok) break;
-                            }
-                            for (int idx = lane; idx < 2 * kTileRows * 8; idx += 32) {
-                                const int hc = idx / (kTileRows * 8);
-                                const int r = (idx / 8) % kTileRows;
-                                const int c16 = idx % 8;
-                                if (r < valid && loaded[r >> 6]) continue;
-                                *reinterpret_cast<uint4 *>(smem + C::OFF_S3 + s * C::VPAIR + hc * C::CHUNK + r * 128 +
-                                                           c16 * 16) = make_uint4(0u, 0u, 0u, 0u);
-                            }
-                            fence_proxy_async_smem();
-                            __syncwarp();
-                            if (lane == 0) arrive0(BR::S3F + s);
+                            tr.put(kEvVPair, (int)g3);
                         }
+                        __syncwarp();
+                    } else {
+                        // a tail: land the valid rows, zero all others, so that whatever the cache (or
+                        // the slot) holds there meets P = 0 as an exact 0
+                        const int nload = (ya[h] >= 0 ? 1 : 0) + (yb[h] >= 0 ? 1 : 0);
+                        if (nload > 0) {
+                            if (lead) {
+                                mbar_arrive_expect_tx(bar(BR::TAIL), 2 * nload * C::HALF);
+                                for (int hc = 0; hc < 2; ++hc) {
+                                    if (ya[h] >= 0)
+                                        tma_load_2d(dst + hc * C::CHUNK, &tm.kv, bar(BR::TAIL), x0 + 64 * hc, ya[h]);
+                                    if (yb[h] >= 0)
+                                        tma_load_2d(dst + hc * C::CHUNK + C::HALF, &tm.kv, bar(BR::TAIL), x0 + 64 * hc,
+                                                    yb[h]);
+                                }
+                            }
+                            __syncwarp();
+                            ok = wait_phase(bar(BR::TAIL), tail_uses & 1, wc, status);
+                            ++tail_uses;
+                            if (!__all_sync(0xffffffffu, ok)) break;
+                        }
+                        for (int idx = lane; idx < 2 * kTileRows * 8; idx += 32) {
+                            const int hc = idx / (kTileRows * 8);
+                            const int r = (idx / 8) % kTileRows;
+                            const int c16 = idx % 8;
+                            if (r < valid[h] && (r < 64 ? ya[h] : yb[h]) >= 0) continue;
+                            *reinterpret_cast<uint4 *>(smem + C::OFF_S3 + s * C::VPAIR + hc * C::CHUNK + r * 128 +
+                                                       c16 * 16) = make_uint4(0u, 0u, 0u, 0u);
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lead) arrive0(BR::S3F + (int)s);
+                        __syncwarp();
                     }
                 }
-            }
-            // Tail: the last slot releases (multicast commits) land before this CTA leaves.
-            for (uint32_t g = g3; ok && g < g3 + C::NS3; ++g) {
-                if (lane == 0) ok = poll_phase(bar(BR::S3E + g % C::NS3), ((g / C::NS3) & 1) ^ 1, wc, status);
-                ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
             }
         }
+        // Tail: the last slot releases (multicast commits) land before this CTA leaves.
+        if (fb < fe)
+            for (uint32_t g = g3; ok && g < g3 + C::NS3; ++g)
+                ok = poll_phase(bar(BR::S3E + (int)(g % C::NS3)), ((g / C::NS3) & 1) ^ 1, wc, status);
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------------------ step-1 issuer (even CTA)
         // Step 1 of each unit chunk by chunk as its K tiles land in both CTAs.
-        if (leader && lane == 0 && fb < fe) {
+        if (leader && fb < fe) {
+            const bool lead = elect_one();
             const uint64_t q_desc0 = smem_desc(sbase + C::OFF_Q, 16, 1024, kSwizzle128B);
             const uint64_t k_desc0 = smem_desc(sbase + C::OFF_S1, 16, 1024, kSwizzle128B);
             TileCursor qc;
             qc.init(tile_off, seq0, fb, fe);
-            int kq = 0, seg_q = 0, qstage = 0;
+            bool ok = true;
+            int kq = 0, seg_q = 0;
             uint32_t g1 = 0;
             TraceRowT<TR> tr;
             tr.init(p, 1);
-            uint64_t t_last = global_timer_ns();
-            while (qc.valid) {
-                bool progressed = false;
+            if (!lead) tr.row = nullptr;
+            while (__all_sync(0xffffffffu, ok && qc.valid)) {
                 const uint32_t d_s = tmem + C::S_COL + (uint32_t)(kq & 1) * NC;
-                if (qstage == 0) {
-                    bool ready = mbar_test_wait_cluster(bar(BR::SE + (kq & 1)), ((kq >> 1) & 1) ^ 1);
-                    if (ready && qc.first()) ready = mbar_test_wait_cluster(bar(BR::QF), seg_q & 1);
-                    if (ready) {
-                        fence_acquire_cluster_smem();
-                        tr.put(kEvS1Begin, kq);
-                        qstage = 1;
-                        progressed = true;
-                    }
-                }
-                if (qstage >= 1) {
-                    const int i = qstage - 1;
-                    const int s = (int)(g1 % C::NS1);
-                    if (mbar_test_wait_cluster(bar(BR::S1F + s), (g1 / C::NS1) & 1)) {
-                        fence_acquire_cluster_smem();
-                        tc_fence_after();
+                ok = poll_phase_cluster(bar(BR::SE + (kq & 1)), ((kq >> 1) & 1) ^ 1, wc, status);
+                if (ok && qc.first()) ok = poll_phase_cluster(bar(BR::QF), seg_q & 1, wc, status);
+                if (!__all_sync(0xffffffffu, ok)) break;
+                tr.put(kEvS1Begin, kq);
+#pragma unroll 1
+                for (uint32_t i = 0; i < 9; ++i, ++g1) {
+                    const uint32_t s = g1 % C::NS1;
+                    ok = poll_phase_cluster(bar(BR::S1F + (int)s), (g1 / C::NS1) & 1, wc, status);
+                    if (!__all_sync(0xffffffffu, ok)) break;
+                    tc_fence_after();
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            // A = K tile chunk (K-major, 128 rows per CTA), B = Q^T chunk (K-major, NH per CTA)
-                            const uint64_t a = k_desc0 + ((uint32_t)(s * C::CHUNK + 32 * j) >> 4);
-                            const uint64_t bq = q_desc0 + ((uint32_t)(i * C::Q_CHUNK + 32 * j) >> 4);
-                            umma_bf16_pair(d_s, a, bq, C::IDESC_S, (i == 0 && j == 0) ? 0u : 1u);
-                        }
-                        umma_commit_pair_both(bar(BR::S1E + s));
-                        tr.put(kEvS1Chunk, i);
-                        ++g1;
-                        progressed = true;
-                        if (++qstage > 9) {
-                            umma_commit_pair_both(bar(BR::SF + (kq & 1)));
-                            tr.put(kEvS1Done, kq);
-                            if (qc.last()) {
-                                umma_commit_pair_both(bar(BR::QE));
-                                ++seg_q;
-                            }
-                            qc.advance(tile_off);
-                            ++kq;
-                            qstage = 0;
-                        }
+                    for (uint32_t j = 0; j < 4; ++j) {
+                        // A = K tile chunk (K-major, 128 rows per CTA), B = Q^T chunk (K-major, NH per CTA)
+                        const uint64_t a = k_desc0 + ((s * C::CHUNK + 32 * j) >> 4);
+                        const uint64_t bq = q_desc0 + ((i * C::Q_CHUNK + 32 * j) >> 4);
+                        umma_bf16_pair_elected(lead, d_s, a, bq, C::IDESC_S, j == 0 ? (i == 0 ? 0u : 1u) : 1u);
                     }
+                    if (lead) umma_commit_pair_both(bar(BR::S1E + (int)s));
+                    __syncwarp();
+                    tr.put(kEvS1Chunk, (int)i);
                 }
-                if (progressed) {
-                    t_last = global_timer_ns();
-                } else if (wc->abort) {
-                    break;
-                } else if (global_timer_ns() - t_last > wc->limit_ns) {
-                    wc->abort = 1;
-                    atomicCAS(status, 0, kStatusTimeout);
-                    break;
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                if (lead) umma_commit_pair_both(bar(BR::SF + (kq & 1)));
+                __syncwarp();
+                tr.put(kEvS1Done, kq);
+                if (__any_sync(0xffffffffu, qc.last())) {
+                    if (lead) umma_commit_pair_both(bar(BR::QE));
+                    __syncwarp();
+                    ++seg_q;
                 }
+                qc.advance(tile_off);
+                ++kq;
             }
             // Tail: both CTAs' last releases of the score buffers (the odd CTA's arrive is remote)
             // land before this CTA leaves.
-            for (int k = kq; k < kq + 2 && !wc->abort; ++k)
-                if (!poll_phase(bar(BR::SE + (k & 1)), ((k >> 1) & 1) ^ 1, wc, status)) break;
-            pv_pending = true;  // FINAL is committed (and drained) at the end of the kernel
+            for (int k = kq; ok && k < kq + 2 && !wc->abort; ++k)
+                ok = poll_phase(bar(BR::SE + (k & 1)), ((k >> 1) & 1) ^ 1, wc, status);
+            pv_pending = lead;  // FINAL is committed (and drained) at the end of the kernel
         }
         __syncwarp();
     } else if (warp == 11) {
@@ -406,83 +425,60 @@ __device__ __forceinline__ void duo_body(const DuoMaps &tm, const DecodeParams &
             // Per unit: K-half 0 once PF0 (both CTAs hold the even CTA's P^T part), value pair by value
             // pair as they land, then PE0; K-half 1 once PF1 and this CTA's XF (the odd CTA's part
             // landed here), then PE1.  Each value slot is freed as its MMAs complete.
-            if (lane == 0 && fb < fe) {
+            if (fb < fe) {
+                const bool lead = elect_one();
                 const uint64_t v_desc0 = smem_desc(sbase + C::OFF_S3, C::CHUNK, 1024, kSwizzle128B);
                 const uint64_t p_desc0 = smem_desc(sbase + C::OFF_P, C::P_BUF, 1024, kSwizzle128B);
                 TileCursor pc;
                 pc.init(tile_off, seq0, fb, fe);
-                int kp = 0, pstage = 0;
-                bool armed = false;
+                bool ok = true;
+                int kp = 0;
                 uint32_t g3 = 0;
                 TraceRowT<TR> tr;
                 tr.init(p, 4);
-                uint64_t t_last = global_timer_ns();
-                while (pc.valid) {
-                    bool progressed = false;
-                    if (!armed) {
-                        mbar_arrive_expect_tx(bar(BR::XF), C::P_BUF);  // the odd CTA's part of unit kp
-                        armed = true;
-                    }
-                    if (pstage == 0 && mbar_test_wait_cluster(bar(BR::PF0), kp & 1)) {
-                        fence_acquire_cluster_smem();
-                        tr.put(kEvPReady, 2 * kp);
-                        pstage = 1;
-                        progressed = true;
-                    } else if (pstage == 3 && mbar_test_wait_cluster(bar(BR::PF1), kp & 1) &&
-                               mbar_test_wait_cluster(bar(BR::XF), kp & 1)) {
-                        fence_acquire_cluster_smem();
-                        fence_proxy_async_smem();  // the st.async writes are read by the tensor core next
-                        tr.put(kEvPReady, 2 * kp + 1);
-                        pstage = 4;
-                        progressed = true;
-                    }
-                    if (pstage != 0 && pstage != 3) {
-                        const int v = pstage <= 2 ? pstage - 1 : pstage - 2;  // value pair 0..3
-                        const int h = v >> 1, j = v & 1;
-                        const int s = (int)(g3 % C::NS3);
-                        if (mbar_test_wait_cluster(bar(BR::S3F + s), (g3 / C::NS3) & 1)) {
-                            fence_acquire_cluster_smem();
-                            tc_fence_after();
-                            const uint32_t d_o = tmem + C::O_COL + (uint32_t)j * C::NP;
-                            const bool init = pc.first() && h == 0;
-#pragma unroll
-                            for (int k8 = 0; k8 < 8; ++k8) {
-                                // A = V^T: M = 128 latent rows of this CTA (two chunks), K = 16 KV rows
-                                const uint64_t a = v_desc0 + ((uint32_t)(s * C::VPAIR + 2048 * k8) >> 4);
-                                // B = P^T of K-half h: K = 16 KV rows, N = this CTA's NPH columns
-                                const uint64_t bp = p_desc0 + ((uint32_t)(h * C::P_BUF + 2048 * k8) >> 4);
-                                umma_bf16_pair(d_o, a, bp, C::IDESC_O, (init && k8 == 0) ? 0u : 1u);
-                            }
-                            umma_commit_pair_both(bar(BR::S3E + s));
-                            tr.put(kEvS3Pair, v);
-                            ++g3;
-                            progressed = true;
-                            if (v == 1) {
-                                umma_commit_pair_both(bar(BR::PE0));
-                                pstage = 3;
-                            } else if (v == 3) {
-                                umma_commit_pair_both(bar(BR::PE1));
-                                tr.put(kEvS3Done, kp);
-                                pc.advance(tile_off);
-                                ++kp;
-                                pstage = 0;
-                                armed = false;
-                            } else {
-                                ++pstage;
-                            }
+                if (!lead) tr.row = nullptr;
+                while (__all_sync(0xffffffffu, ok && pc.valid)) {
+                    if (lead) mbar_arrive_expect_tx(bar(BR::XF), C::P_BUF);  // the odd CTA's part of unit kp
+                    __syncwarp();
+                    const uint32_t fresh = __any_sync(0xffffffffu, pc.first()) ? 0u : 1u;
+#pragma unroll 1
+                    for (uint32_t h = 0; h < 2; ++h) {
+                        ok = poll_phase_cluster(bar(h == 0 ? BR::PF0 : BR::PF1), kp & 1, wc, status);
+                        if (ok && h == 1) {
+                            ok = poll_phase_cluster(bar(BR::XF), kp & 1, wc, status);
+                            fence_proxy_async_smem();  // the st.async writes are read by the tensor core next
                         }
+                        if (!__all_sync(0xffffffffu, ok)) break;
+                        tr.put(kEvPReady, 2 * kp + (int)h);
+#pragma unroll 1
+                        for (uint32_t j = 0; j < 2; ++j, ++g3) {
+                            const uint32_t s = g3 % C::NS3;
+                            ok = poll_phase_cluster(bar(BR::S3F + (int)s), (g3 / C::NS3) & 1, wc, status);
+                            if (!__all_sync(0xffffffffu, ok)) break;
+                            tc_fence_after();
+                            const uint32_t d_o = tmem + C::O_COL + j * C::NP;
+#pragma unroll
+                            for (uint32_t k8 = 0; k8 < 8; ++k8) {
+                                // A = V^T: M = 128 latent rows of this CTA (two chunks), K = 16 KV rows
+                                const uint64_t a = v_desc0 + ((s * C::VPAIR + 2048 * k8) >> 4);
+                                // B = P^T of K-half h: K = 16 KV rows, N = this CTA's NPH columns
+                                const uint64_t bp = p_desc0 + ((h * C::P_BUF + 2048 * k8) >> 4);
+                                umma_bf16_pair_elected(lead, d_o, a, bp, C::IDESC_O, k8 == 0 ? (h == 0 ? fresh : 1u) : 1u);
+                            }
+                            if (lead) umma_commit_pair_both(bar(BR::S3E + (int)s));
+                            __syncwarp();
+                            tr.put(kEvS3Pair, (int)(2 * h + j));
+                        }
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok) break;
+                        if (lead) umma_commit_pair_both(bar(h == 0 ? BR::PE0 : BR::PE1));
+                        __syncwarp();
                     }
-                    if (progressed) {
-                        t_last = global_timer_ns();
-                    } else if (wc->abort) {
-                        break;
-                    } else if (global_timer_ns() - t_last > wc->limit_ns) {
-                        wc->abort = 1;
-                        atomicCAS(status, 0, kStatusTimeout);
-                        break;
-                    }
+                    tr.put(kEvS3Done, kp);
+                    pc.advance(tile_off);
+                    ++kp;
                 }
-                pv_pending = true;  // FINAL3 is committed (and drained) at the end of the kernel
+                pv_pending = lead;  // FINAL3 is committed (and drained) at the end of the kernel
             }
         } else if (lane == 0 && fb < fe) {
             // -------------------------------------------------------- relay (odd CTA)
@@ -959,7 +955,7 @@ __global__ void __launch_bounds__(kDuoThreads, 1)
     tc_fence_before();
     cluster_sync();  // both CTAs' barriers and TMEM exist before any remote operation
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);  // (known to be the same in all lanes)
     // Launched as a programmatic dependent of the plan: nothing above read global memory.
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

@@ -17,6 +17,7 @@
 #include "api_common.h"
 #include "etap_pair_kernel.cuh"
 #include "etap_duo_kernel.cuh"
+#include "etap_wide8_kernel.cuh"
 #include "plan_combine_kernels.cuh"
 #include "untransposed_kernel.cuh"
 #include "plan_core.h"
@@ -131,8 +132,8 @@ int ensure_smem_attr() {
         e = cudaFuncSetAttribute(mla::etap_pair_kernel<mla::PairCfg16E4, false, true>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize, (int)mla::PairCfg16E4::SMEM_ALLOC);
         if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
-        e = cudaFuncSetAttribute(mla::etap_pair_kernel<mla::PairCfg32E4, false, true>,
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, (int)mla::PairCfg32E4::SMEM_ALLOC);
+        e = cudaFuncSetAttribute(mla::etap_wide8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)mla::Wide8::SMEM_ALLOC);
         if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
         e = cudaFuncSetAttribute(mla::etap_duo_kernel<mla::DuoCfg64, mla::DuoCfg128, false, true>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize, (int)mla::kDuoSmemAlloc);
@@ -166,8 +167,11 @@ cudaError_t launch_pair(const CUtensorMap &tm_q, const CUtensorMap &tm_kv, const
     if constexpr (!C::KV8) {
         if (p.trace) return cudaLaunchKernelEx(&cfg, mla::etap_pair_kernel<C, true>, tm_q, tm_kv, tm_qr, tm_kvr, p);
     }
-    if (p.tree_mask)
-        return cudaLaunchKernelEx(&cfg, mla::etap_pair_kernel<C, false, true>, tm_q, tm_kv, tm_qr, tm_kvr, p);
+    // (the tree form of more than 16 columns of an E4M3 cache is launch_wide8)
+    if constexpr (C::NG == 16) {
+        if (p.tree_mask)
+            return cudaLaunchKernelEx(&cfg, mla::etap_pair_kernel<C, false, true>, tm_q, tm_kv, tm_qr, tm_kvr, p);
+    }
     return cudaLaunchKernelEx(&cfg, mla::etap_pair_kernel<C>, tm_q, tm_kv, tm_qr, tm_kvr, p);
 }
 
@@ -192,6 +196,26 @@ cudaError_t launch_duo(const mla::DuoMaps &maps, const mla::DecodeParams &p, int
     if (p.tree_mask)
         return cudaLaunchKernelEx(&cfg, mla::etap_duo_kernel<mla::DuoCfg64, mla::DuoCfg128, false, true>, maps, p);
     return cudaLaunchKernelEx(&cfg, mla::etap_duo_kernel<mla::DuoCfg64, mla::DuoCfg128>, maps, p);
+}
+
+// The E4M3 cache's tree decode of more than 16 columns, on the duo kernel's grid.
+cudaError_t launch_wide8(const CUtensorMap &tm_kv, const CUtensorMap &tm_kvr, const mla::DecodeParams &p, int clusters,
+                         cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * clusters, 1, 1);
+    cfg.blockDim = dim3(mla::Wide8::THREADS, 1, 1);
+    cfg.dynamicSmemBytes = mla::Wide8::SMEM_ALLOC;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, mla::etap_wide8_kernel, tm_kv, tm_kvr, p);
 }
 
 // The combine kernel, launched as a programmatic dependent of what precedes it on the stream:
@@ -329,7 +353,7 @@ int mla_decode_plan(const int32_t *seqlens, int batch, int q_len, int num_heads,
     // Programmatic dependent launch: the plan is scheduled while the preceding kernel drains
     // and waits for it to complete before its first global read.
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(1, 1, 1);
+    cfg.gridDim = dim3(lay.has_duo ? 2 : 1, 1, 1);  // a CTA per schedule
     cfg.blockDim = dim3(mla::kPlanThreads, 1, 1);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
@@ -406,6 +430,8 @@ int decode_fwd_impl(const void *q, const void *kv, const float *kv_scale, const 
     const uint64_t kv_total_rows = paged ? (uint64_t)kv_rows : (uint64_t)batch * kv_rows;
     // the bf16 cache with more than 16 query columns runs the M = 256 kernel on the duo schedule
     const bool duo = !fp8 && lay.has_duo;
+    // a tree on the E4M3 cache with more than 16 columns runs its own kernel on the same schedule
+    const bool wide8 = fp8 && tree_mask && lay.has_duo;
     if (fp8) {
         // the E4M3 kernel quantises Q itself (no Q maps): 128-code boxes of the latent part, 64-code rope boxes
         st = encode_rows_576(&tm_kv, kv, kv_total_rows, 64, 128, 1);
@@ -506,14 +532,16 @@ int decode_fwd_impl(const void *q, const void *kv, const float *kv_scale, const 
         if (flags & MLA_FLAG_SKIP_COMBINE) return MLA_OK;
         return launch_combine(workspace, batch, q_len, num_heads, num_sms, o, lse, 0, p.wait_limit_ns, s);
     }
-    if (duo) {
+    if (duo || wide8) {
         mla::DuoMaps maps;
-        st = encode_rows_576(&maps.q32, q, (uint64_t)batch * ncols, 32);
-        if (st != MLA_OK) return st;
-        st = encode_rows_576(&maps.q64, q, (uint64_t)batch * ncols, 64);
-        if (st != MLA_OK) return st;
-        st = encode_rows_576(&maps.kv, kv, kv_total_rows, 64);
-        if (st != MLA_OK) return st;
+        if (duo) {
+            st = encode_rows_576(&maps.q32, q, (uint64_t)batch * ncols, 32);
+            if (st != MLA_OK) return st;
+            st = encode_rows_576(&maps.q64, q, (uint64_t)batch * ncols, 64);
+            if (st != MLA_OK) return st;
+            st = encode_rows_576(&maps.kv, kv, kv_total_rows, 64);
+            if (st != MLA_OK) return st;
+        }
         // the plan picks the grouping on the device (see plan_core.h); the kernel reads it from the header
         p.ctas = lay.duo.ctas_max;
         p.groups = lay.duo.groups_max;
@@ -532,10 +560,11 @@ int decode_fwd_impl(const void *q, const void *kv, const float *kv_scale, const 
             const int g = mla::duo_groups(ncols, mode), c = mla::num_ctas(num_sms, g) * g;
             if (c > clusters) clusters = c;
         }
-        e = launch_duo(maps, p, clusters, s);
-        if (e != cudaSuccess) return cuda_fail(e, "etap_duo_kernel launch");
+        const char *what = duo ? "etap_duo_kernel launch" : "etap_wide8_kernel launch";
+        e = duo ? launch_duo(maps, p, clusters, s) : launch_wide8(tm_kv, tm_kvr, p, clusters, s);
+        if (e != cudaSuccess) return cuda_fail(e, what);
         e = cudaGetLastError();
-        if (e != cudaSuccess) return cuda_fail(e, "etap_duo_kernel launch");
+        if (e != cudaSuccess) return cuda_fail(e, what);
         if (flags & MLA_FLAG_SKIP_COMBINE) return MLA_OK;
         return launch_combine(workspace, batch, q_len, num_heads, num_sms, o, lse, 1, p.wait_limit_ns, s);
     }
