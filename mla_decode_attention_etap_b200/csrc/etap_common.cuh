@@ -32,6 +32,10 @@ constexpr float kRescaleThreshold8 = 4.0f;
 constexpr float kRescaleHeadroom8 = 2.0f;
 constexpr float kPScaleLog2_8 = 4.0f;
 
+// Minus the running maximum of a column that has seen no row: far above minus any score, and finite, so
+// that a masked score (-inf) plus it is -inf and any other passes the threshold.
+constexpr float kNoRow = 1e30f;
+
 // Per-CTA wait control in shared memory: the abort flag every role polls and
 // the bound after which a wait gives up.
 struct WaitCtl {

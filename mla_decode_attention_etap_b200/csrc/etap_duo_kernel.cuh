@@ -50,8 +50,10 @@ constexpr uint32_t kDuoCtlMx = 4096;      // float[128] peer's tile maxima (rece
 constexpr uint32_t kDuoCtlLx = 4608;      // float[128] peer's row sums (received)
 constexpr uint32_t kDuoCtlMt = 5120;      // float[128] this CTA's tile maxima / row sums
 constexpr uint32_t kDuoCtlVis = 5632;     // int[128] visible rows per column of the current sequence
-constexpr uint32_t kDuoCtlEnd = 6144;     // data regions start here (1024-aligned)
+constexpr uint32_t kDuoCtlNm = 6144;      // float[128] minus the running maximum (kNoRow: no row seen yet)
+constexpr uint32_t kDuoCtlEnd = 7168;     // data regions start here (1024-aligned)
 constexpr int kDuoThreads = 384;
+constexpr int kDuoMaxSlots = 4;           // slots per operand ring that have barriers
 
 // NC query columns per cluster, P as hi + lo (SPLIT), NS1 K-chunk slots, NS3 value-pair slots.
 template <int NC_, bool SPLIT_, int NS1_, int NS3_>
@@ -78,27 +80,31 @@ struct DuoCfg {
     static constexpr uint32_t IDESC_S = idesc_bf16_f32(256, NC, 0, 0);
     static constexpr uint32_t IDESC_O = idesc_bf16_f32(256, NP, 1, 1);
 };
-using DuoCfg64 = DuoCfg<64, true, 3, 3>;     // 64 columns, P as bf16 hi + lo
+// Ring slots, measured: 64 columns at B=16, q_len*h=64, 32768 rows: 4 K chunks + 2 value pairs 163 us, 3 + 3
+// 170 us, 5 + 2 166 us, and with value slots of half the size 4 + 5 164 us; 128 columns at B=8, h=128,
+// q_len=4: 3 + 2 208 us, 5 + 1 233 us, half-size slots 3 + 4 217 us.
+using DuoCfg64 = DuoCfg<64, true, 4, 2>;     // 64 columns, P as bf16 hi + lo
 using DuoCfg128 = DuoCfg<128, false, 3, 2>;  // 128 columns, one bf16 P term
 constexpr uint32_t kDuoSmemAlloc =
     (DuoCfg64::BYTES > DuoCfg128::BYTES ? DuoCfg64::BYTES : DuoCfg128::BYTES) + 1024;  // + alignment slack
 
 template <class C>
 constexpr bool duo_cfg_fits() {
-    return C::BYTES + 1024 <= 232448 && kDuoCtlVis + 512 <= kDuoCtlEnd && C::S_COL + 2 * C::NC <= 512 && C::P_PITCH == 128 && C::NS1 <= 3 &&
-           C::NS3 <= 3 && C::OFF_Q % 1024 == 0 && C::OFF_P % 1024 == 0 && C::NC <= 128 && C::NH % 16 == 0;
+    return C::BYTES + 1024 <= 232448 && kDuoCtlNm + 512 <= kDuoCtlEnd && C::S_COL + 2 * C::NC <= 512 && C::P_PITCH == 128 &&
+           C::NS1 <= kDuoMaxSlots && C::NS3 <= kDuoMaxSlots && C::OFF_Q % 1024 == 0 && C::OFF_P % 1024 == 0 && C::NC <= 128 && C::NH % 16 == 0;
 }
 static_assert(duo_cfg_fits<DuoCfg64>() && duo_cfg_fits<DuoCfg128>(), "shared memory / TMEM plan");
 
-// Barrier indices (the same in both configurations; slot barriers sized for 3 slots).  Barriers
+// Barrier indices (the same in both configurations; slot barriers sized for kDuoMaxSlots slots).  Barriers
 // that gather both CTAs (S1F, S3F, QF, SE, PF0, PF1) are used in the even CTA only.  Step 3 runs in
 // two K-halves: K-half h reads the P^T buffers that CTA h's softmax fills (its own columns in place,
 // the peer's columns through st.async), so PF_h / PE_h track them separately and CTA h refills
 // them as soon as the previous unit's K-half h is done.
 struct DuoBars {
-    static constexpr int S1F = 0, S1E = 3, S3F = 6, S3E = 9, QF = 12, QE = 13, SF = 14, SE = 16, PF0 = 18, PF1 = 19,
-                         PE0 = 20, PE1 = 21, XF = 22, XV = 23, XM = 24, XL = 25, TAIL = 26, FINAL = 27, FINAL3 = 28,
-                         COUNT = 29;
+    static constexpr int S1F = 0, S1E = S1F + kDuoMaxSlots, S3F = S1E + kDuoMaxSlots, S3E = S3F + kDuoMaxSlots,
+                         QF = S3E + kDuoMaxSlots, QE = QF + 1, SF = QF + 2, SE = QF + 4, PF0 = QF + 6, PF1 = QF + 7,
+                         PE0 = QF + 8, PE1 = QF + 9, XF = QF + 10, XV = QF + 11, XM = QF + 12, XL = QF + 13,
+                         TAIL = QF + 14, FINAL = QF + 15, FINAL3 = QF + 16, COUNT = QF + 17;
 };
 static_assert(DuoBars::COUNT * 8 <= kDuoCtlMisc, "barrier area");
 
@@ -525,6 +531,7 @@ __device__ __forceinline__ void duo_body(const DuoMaps &tm, const DecodeParams &
         const uint32_t lane_addr = (uint32_t)(quad * 32) << 16;
         const bool own = half == (int)rank;       // these columns are this CTA's half of step 3's B operand
         float *m_s = reinterpret_cast<float *>(smem + kDuoCtlM);
+        float *nm_s = reinterpret_cast<float *>(smem + kDuoCtlNm);
         float *alpha_s = reinterpret_cast<float *>(smem + kDuoCtlAlpha);
         float *red = reinterpret_cast<float *>(smem + kDuoCtlRed);
         const float *mx = reinterpret_cast<const float *>(smem + kDuoCtlMx);
@@ -554,22 +561,27 @@ __device__ __forceinline__ void duo_body(const DuoMaps &tm, const DecodeParams &
         uint32_t seen[NH / 32] = {};  // TREE: bit n of word cc: column 32 cc + n of this half sees this thread's row
         auto load_scores = [&](int cc, bool full, int rg, float (&x)[32]) {
             tmem_ld32_wait(tmem + lane_addr + C::S_COL + (uint32_t)(k & 1) * NC + half * NH + 32 * cc, x);
-            if (full) {
+            const float2 sc = make_float2(p.scale_log2, p.scale_log2);
 #pragma unroll
-                for (int n = 0; n < 32; ++n) x[n] *= p.scale_log2;
-            } else if constexpr (TREE) {
+            for (int n = 0; n < 32; n += 2) {
+                const float2 v = mul2(make_float2(x[n], x[n + 1]), sc);
+                x[n] = v.x;
+                x[n + 1] = v.y;
+            }
+            if (full) return;
+            if constexpr (TREE) {
                 const uint32_t bits = cc == 0 ? seen[0] : seen[NH / 32 - 1];
 #pragma unroll
-                for (int n = 0; n < 32; ++n) x[n] = (bits >> n) & 1u ? x[n] * p.scale_log2 : -INFINITY;
+                for (int n = 0; n < 32; ++n) x[n] = (bits >> n) & 1u ? x[n] : -INFINITY;
             } else {
                 const int4 *v4 = reinterpret_cast<const int4 *>(vis_s + half * NH + 32 * cc);
 #pragma unroll
                 for (int q = 0; q < 8; ++q) {
                     const int4 vv = v4[q];
-                    x[4 * q] = rg < vv.x ? x[4 * q] * p.scale_log2 : -INFINITY;
-                    x[4 * q + 1] = rg < vv.y ? x[4 * q + 1] * p.scale_log2 : -INFINITY;
-                    x[4 * q + 2] = rg < vv.z ? x[4 * q + 2] * p.scale_log2 : -INFINITY;
-                    x[4 * q + 3] = rg < vv.w ? x[4 * q + 3] * p.scale_log2 : -INFINITY;
+                    x[4 * q] = rg < vv.x ? x[4 * q] : -INFINITY;
+                    x[4 * q + 1] = rg < vv.y ? x[4 * q + 1] : -INFINITY;
+                    x[4 * q + 2] = rg < vv.z ? x[4 * q + 2] : -INFINITY;
+                    x[4 * q + 3] = rg < vv.w ? x[4 * q + 3] : -INFINITY;
                 }
             }
         };
@@ -582,28 +594,31 @@ __device__ __forceinline__ void duo_body(const DuoMaps &tm, const DecodeParams &
             for (int cc = 0; cc < NH / 32; ++cc) {
                 float x[32];
                 load_scores(cc, full, rg, x);
-                const float4 *m4 = reinterpret_cast<const float4 *>(m_s + half * NH + 32 * cc);
+                const float4 *nm4 = reinterpret_cast<const float4 *>(nm_s + half * NH + 32 * cc);
                 // one 16-byte chunk (8 columns) at a time: hi at chunk 4cc+u, lo (split) at NH/8 + that
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
                     uint32_t hi[4], lo[4];
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
-                        const float4 mm = m4[2 * u + q];
-                        const float mv[4] = {mm.x == -INFINITY ? 0.f : mm.x, mm.y == -INFINITY ? 0.f : mm.y,
-                                             mm.z == -INFINITY ? 0.f : mm.z, mm.w == -INFINITY ? 0.f : mm.w};
+                        const float4 nm = nm4[2 * u + q];
 #pragma unroll
                         for (int e = 0; e < 4; e += 2) {
                             const int n = 8 * u + 4 * q + e;
-                            const float p0 = fast_exp2(x[n] - mv[e]);
-                            const float p1 = fast_exp2(x[n + 1] - mv[e + 1]);
-                            lpart[32 * cc + n] += p0;
-                            lpart[32 * cc + n + 1] += p1;
-                            const __nv_bfloat16 h0 = __float2bfloat16_rn(p0), h1 = __float2bfloat16_rn(p1);
-                            hi[2 * q + e / 2] =
-                                (uint32_t)__bfloat16_as_ushort(h0) | ((uint32_t)__bfloat16_as_ushort(h1) << 16);
-                            if constexpr (C::SPLIT)
-                                lo[2 * q + e / 2] = pack_bf16x2(p0 - __bfloat162float(h0), p1 - __bfloat162float(h1));
+                            const float2 d = add2(make_float2(x[n], x[n + 1]),
+                                                  e == 0 ? make_float2(nm.x, nm.y) : make_float2(nm.z, nm.w));
+                            const float2 pv = make_float2(fast_exp2(d.x), fast_exp2(d.y));
+                            const float2 l = add2(make_float2(lpart[32 * cc + n], lpart[32 * cc + n + 1]), pv);
+                            lpart[32 * cc + n] = l.x;
+                            lpart[32 * cc + n + 1] = l.y;
+                            const uint32_t h = pack_bf16x2(pv.x, pv.y);
+                            hi[2 * q + e / 2] = h;
+                            if constexpr (C::SPLIT) {
+                                // p - hi, exactly rounded as a subtraction
+                                const float2 r = fma2(make_float2(__uint_as_float(h << 16), __uint_as_float(h & 0xFFFF0000u)),
+                                                      make_float2(-1.f, -1.f), pv);
+                                lo[2 * q + e / 2] = pack_bf16x2(r.x, r.y);
+                            }
                         }
                     }
 #pragma unroll
@@ -651,6 +666,7 @@ __device__ __forceinline__ void duo_body(const DuoMaps &tm, const DecodeParams &
                     }
                     vis_s[tid] = vis;
                     m_s[tid] = -INFINITY;
+                    nm_s[tid] = kNoRow;
                 }
                 named_bar_sync(SMX, NSM);
 #pragma unroll
@@ -677,20 +693,22 @@ __device__ __forceinline__ void duo_body(const DuoMaps &tm, const DecodeParams &
                                grp * NC + NC <= p.ncols;
                     }
                     // ---- pass 1: does any score exceed its column's running maximum by > 2^THRESH?
-                    bool need = first || !ok;
+                    float over = -INFINITY;
                     // rolled: one copy of the score read and test (instruction cache; measured faster)
 #pragma unroll 1
                     for (int cc = 0; cc < NH / 32; ++cc) {
                         float x[32];
                         load_scores(cc, full, rg, x);
-                        const float4 *m4 = reinterpret_cast<const float4 *>(m_s + half * NH + 32 * cc);
+                        const float4 *nm4 = reinterpret_cast<const float4 *>(nm_s + half * NH + 32 * cc);
 #pragma unroll
                         for (int q = 0; q < 8; ++q) {
-                            const float4 mm = m4[q];
-                            need |= (x[4 * q] > mm.x + kRescaleThreshold) | (x[4 * q + 1] > mm.y + kRescaleThreshold) |
-                                    (x[4 * q + 2] > mm.z + kRescaleThreshold) | (x[4 * q + 3] > mm.w + kRescaleThreshold);
+                            const float4 nm = nm4[q];
+                            const float2 d0 = add2(make_float2(x[4 * q], x[4 * q + 1]), make_float2(nm.x, nm.y));
+                            const float2 d1 = add2(make_float2(x[4 * q + 2], x[4 * q + 3]), make_float2(nm.z, nm.w));
+                            over = fmaxf(over, fmaxf(fmaxf(d0.x, d0.y), fmaxf(d1.x, d1.y)));
                         }
                     }
+                    const bool need = first || !ok || over > kRescaleThreshold;
                     const bool vote = named_bar_or(SMX, NSM, need);
                     // ---- votes of both CTAs (a small exchange ahead of P^T, so that P^T is final when written)
                     if (tid == 0) {
@@ -738,10 +756,12 @@ __device__ __forceinline__ void duo_body(const DuoMaps &tm, const DecodeParams &
                             float a = 1.f;
                             if (mo == -INFINITY) {
                                 m_s[tid] = mtot == -INFINITY ? -INFINITY : mtot + kRescaleHeadroom;
+                                nm_s[tid] = mtot == -INFINITY ? kNoRow : -(mtot + kRescaleHeadroom);
                             } else if (mtot > mo + kRescaleThreshold) {
                                 const float mn = mtot + kRescaleHeadroom;
                                 a = fast_exp2(mo - mn);
                                 m_s[tid] = mn;
+                                nm_s[tid] = -mn;
                                 resc = true;
                             }
                             alpha_s[tid] = a;
@@ -914,7 +934,7 @@ __global__ void __launch_bounds__(kDuoThreads, 1)
     if (span && threadIdx.x == 0) span[0] = global_timer_ns();
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < 3; ++i) {
+        for (int i = 0; i < kDuoMaxSlots; ++i) {
             mbar_init(bar(BR::S1F + i), 2);  // both CTAs' producers (expect_tx) + their TMA bytes
             mbar_init(bar(BR::S1E + i), 1);  // the MMA commit
             mbar_init(bar(BR::S3F + i), 2);

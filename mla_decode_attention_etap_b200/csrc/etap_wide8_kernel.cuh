@@ -27,10 +27,6 @@
 
 namespace mla {
 
-// Minus the running maximum of a column that has seen no row: far above minus any score, and finite, so
-// that a masked score (-inf) plus it is -inf and any other passes the threshold.
-constexpr float kNoRow = 1e30f;
-
 struct Wide8 {
     static constexpr int NC = 64;                      // query columns of a CTA
     static constexpr int NV = 8;                       // 16 KB slots: 128 rows x 128 codes
