@@ -32,15 +32,48 @@ __device__ __forceinline__ int64_t block_exclusive_scan(int64_t x, int64_t *smem
     return base + incl - x;
 }
 
+// The same for two values at once (smem64: 64 words).
+__device__ __forceinline__ void block_exclusive_scan2(int64_t &x, int64_t &y, int64_t *smem64, int64_t *total_x,
+                                                      int64_t *total_y) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarps = blockDim.x >> 5;
+    int64_t ix = x, iy = y;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int64_t a = __shfl_up_sync(0xffffffffu, ix, d), b = __shfl_up_sync(0xffffffffu, iy, d);
+        if (lane >= d) {
+            ix += a;
+            iy += b;
+        }
+    }
+    if (lane == 31) {
+        smem64[warp] = ix;
+        smem64[32 + warp] = iy;
+    }
+    __syncthreads();
+    if (warp < 2) {  // one warp per value
+        int64_t w = lane < nwarps ? smem64[32 * warp + lane] : 0;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int64_t a = __shfl_up_sync(0xffffffffu, w, d);
+            if (lane >= d) w += a;
+        }
+        smem64[32 * warp + lane] = w;  // inclusive prefix of the warp sums
+    }
+    __syncthreads();
+    x = (warp > 0 ? smem64[warp - 1] : 0) + ix - x;
+    y = (warp > 0 ? smem64[32 + warp - 1] : 0) + iy - y;
+    *total_x = smem64[nwarps - 1];
+    *total_y = smem64[32 + nwarps - 1];
+    __syncthreads();  // smem64 is free for the next scan
+}
+
 // Minimum of one int per thread over the block (all threads call it).
 __device__ __forceinline__ int block_min(int x, int *smem32) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarps = blockDim.x >> 5;
-#pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) x = min(x, __shfl_xor_sync(0xffffffffu, x, d));
+    x = __reduce_min_sync(0xffffffffu, x);
     if (lane == 0) smem32[warp] = x;
     __syncthreads();
-    int r = smem32[0];
-    for (int w = 1; w < nwarps; ++w) r = min(r, smem32[w]);
+    const int r = __reduce_min_sync(0xffffffffu, lane < nwarps ? smem32[lane] : 0x7fffffff);
     __syncthreads();
     return r;
 }

@@ -93,6 +93,80 @@ __device__ void plan_schedule(const int32_t *__restrict__ seqlens, int batch, in
     }
 }
 
+// The same tables for up to kPlanThreads sequences (thread b owns sequence b, of length L) and work
+// units: lengths and offsets stay in registers and shared memory, and the range starts are found by a
+// thread per range (a search for the sequence that holds its cost position) instead of by the
+// sequence's thread, range after range.
+struct PlanSmem {
+    int64_t scan[64];
+    int64_t f[kPlanThreads], g[kPlanThreads];  // first flattened unit, first cost position
+    int32_t start[kPlanThreads + 1];           // first flattened unit of each range
+};
+__device__ void plan_schedule_small(int L, int batch, int ctas, int groups, int unit_rows, int gcols, int mode,
+                                    int32_t *__restrict__ ws, const Sched &sc, int hdr, PlanSmem &sm) {
+    const int b = threadIdx.x, c = threadIdx.x;
+    const int E = end_cost_units(unit_rows);
+    const bool is_seq = b < batch;
+    const int64_t units = is_seq ? units_of(L, unit_rows) : 0;
+    int64_t f = units, g = units + (units > 0 ? E : 0), total, total_cost;
+    block_exclusive_scan2(f, g, sm.scan, &total, &total_cost);
+    const int used = used_ctas(total, ctas);
+    sm.f[b] = f;
+    sm.g[b] = g;
+    // the last of the sequences whose offset is at most x (those without units share their successor's)
+    auto find = [&](const int64_t *off, int64_t x) -> int {
+        int lo = 0, hi = batch;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (off[mid] <= x)
+                lo = mid;
+            else
+                hi = mid;
+        }
+        return lo;
+    };
+    int first = -1, nsplit = 0;
+    if (units > 0) {
+        first = cta_of(total_cost, used, g);
+        nsplit = cta_of(total_cost, used, g + units - 1) - first + 1;
+    }
+    int64_t slot = nsplit >= 2 ? nsplit : 0, slots;
+    slot = block_exclusive_scan(slot, sm.scan, &slots);  // (its barriers publish f and g)
+    if (c < ctas) {
+        int64_t s = total;
+        if (c < used) {
+            const int64_t x = cta_begin(total_cost, used, c);
+            const int q = find(sm.g, x);
+            const int64_t end = q + 1 < batch ? sm.f[q + 1] : total;
+            s = unit_at_cost(x, sm.g[q], sm.f[q], end - sm.f[q]);
+        }
+        sm.start[c] = (int32_t)s;
+    }
+    if (c == 0) sm.start[ctas] = (int32_t)total;
+    __syncthreads();
+    int32_t *counters = ws + sc.counters / 4;
+    if (is_seq) {
+        ws[sc.tile_off / 4 + b] = (int32_t)f;
+        reinterpret_cast<int4 *>(ws + sc.seq_info / 4)[b] = make_int4((int)units, first, nsplit, (int)slot);
+        ws[sc.done / 4 + b] = 0;
+    }
+    if (c < ctas) {
+        const int32_t s = sm.start[c], e = sm.start[c + 1];
+        reinterpret_cast<int2 *>(ws + sc.cta_ranges / 4)[c] = make_int2(s, e);
+        ws[sc.cta_seq / 4 + c] = s < e ? find(sm.f, s) : batch;
+    }
+    for (int i = threadIdx.x; i < 2 * batch * groups; i += kPlanThreads) counters[i] = 0;
+    if (threadIdx.x == 0) {
+        ws[sc.tile_off / 4 + batch] = (int32_t)total;
+        ws[hdr + kSchCtas] = ctas;
+        ws[hdr + kSchGroups] = groups;
+        ws[hdr + kSchTotal] = (int32_t)total;
+        ws[hdr + kSchSlotsUsed] = (int32_t)slots;
+        ws[hdr + kSchGroupCols] = gcols;
+        ws[hdr + kSchMode] = mode;
+    }
+}
+
 // A CTA of kPlanThreads threads per schedule: CTA 0 the pair schedule, and, for more than 16 query
 // columns, CTA 1 the duo schedule (whose column-group width depends on the shortest nonempty sequence).
 // The schedules share no table, so the CTAs run side by side (B=16, q_len=4, h=16: 9.5 us one after the
@@ -106,25 +180,31 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int32_t *__res
     // turn before reading the workspace.  Both are no-ops without programmatic launch.
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    __shared__ int64_t scan_smem[32];
+    __shared__ PlanSmem sm;
     __shared__ int min_smem[32];
     const int per = (batch + kPlanThreads - 1) / kPlanThreads;
     const int b0 = min(batch, (int)threadIdx.x * per), b1 = min(batch, b0 + per);
-    if (blockIdx.x == 0) {
-        plan_schedule(seqlens, batch, b0, b1, lay.ctas, lay.groups, kTileRows, group_cols(ncols), 0, ws, lay.pair,
-                      kHdrPair, scan_smem);
-    } else {
-        int mn = 0x7fffffff;
-        for (int b = b0; b < b1; ++b) {
-            const int L = seqlens[b];
-            if (L > 0) mn = min(mn, L);
-        }
-        mn = block_min(mn, min_smem);
-        const int mode = duo_mode(ncols, mn == 0x7fffffff ? 0 : mn);
-        const int groups = duo_groups(ncols, mode);
-        plan_schedule(seqlens, batch, b0, b1, num_ctas(num_sms, groups), groups, kDuoRows, duo_group_cols(mode), mode,
-                      ws, lay.duo, kHdrDuo, scan_smem);
+    int mn = 0x7fffffff;  // this thread's shortest nonempty sequence
+    for (int b = b0; b < b1; ++b) {
+        const int L = seqlens[b];
+        if (L > 0) mn = min(mn, L);
     }
+    const int L = per == 1 && b0 < b1 && mn != 0x7fffffff ? mn : 0;  // its only sequence
+    int ctas = lay.ctas, groups = lay.groups, mode = 0;
+    if (blockIdx.x == 1) {
+        mn = block_min(mn, min_smem);
+        mode = duo_mode(ncols, mn == 0x7fffffff ? 0 : mn);
+        groups = duo_groups(ncols, mode);
+        ctas = num_ctas(num_sms, groups);
+    }
+    const Sched &sc = blockIdx.x == 0 ? lay.pair : lay.duo;
+    const int hdr = blockIdx.x == 0 ? kHdrPair : kHdrDuo;
+    const int unit_rows = blockIdx.x == 0 ? kTileRows : kDuoRows;
+    const int gcols = blockIdx.x == 0 ? group_cols(ncols) : duo_group_cols(mode);
+    if (per == 1 && ctas <= kPlanThreads)
+        plan_schedule_small(L, batch, ctas, groups, unit_rows, gcols, mode, ws, sc, hdr, sm);
+    else
+        plan_schedule(seqlens, batch, b0, b1, ctas, groups, unit_rows, gcols, mode, ws, sc, hdr, sm.scan);
     if (blockIdx.x == 0 && threadIdx.x == 0) {
         ws[kHdrStatus] = 0;
         ws[kHdrBatch] = batch;
