@@ -392,15 +392,18 @@ __global__ void __launch_bounds__(Wide8::THREADS, 1)
         WideTiles w;
         w.valid = false;
         if (fb < fe) w.init(tile_off, seq0, fb, fe, (int)rank, mode, seq_len);
-        // the scale of this thread's row of a tile (1 for rows that are not loaded)
-        auto row_scale = [&](const WideTiles &at) -> float {
-            if (!at.valid) return 1.f;
+        // The scale of this thread's row of a tile (1 for rows that are not loaded), in two steps so that
+        // neither load is waited for: the row's page, then what stands there.
+        auto page_of = [&](const WideTiles &at) -> int {
             const int rg = at.t * kTileRows + row;
-            if (rg >= at.L) return 1.f;
-            const int y = locate(at.b, rg & ~63);
-            return y < 0 ? 1.f : fmaxf(__ldg(p.kv_scale + (int64_t)y + (rg & 63)), 0x1p-100f);
+            return p.paged && at.valid && rg < at.L ? __ldg(p.block_table + (int64_t)at.b * p.max_blocks + (rg >> 6)) : 0;
         };
-        float sig_next = row_scale(w);
+        auto read_scale = [&](const WideTiles &at, int page) -> float {
+            const int rg = at.t * kTileRows + row;
+            if (!at.valid || rg >= at.L || page < 0 || (int64_t)page * kPage >= p.kv_rows) return 1.f;
+            return __ldg(p.kv_scale + (p.paged ? (int64_t)page * kPage + (rg & 63) : (int64_t)at.b * p.kv_rows + rg));
+        };
+        float sig_next = read_scale(w, page_of(w));
         while (!stop && w.valid) {
             // ---- one segment: tiles of sequence b
             const int b = w.b, L = w.L;
@@ -496,12 +499,12 @@ __global__ void __launch_bounds__(Wide8::THREADS, 1)
             for (; more; ++k) {
                 const bool first = w.first;
                 const int rg = w.t * kTileRows + row;
-                const float sig = sig_next;
+                const float sig = fmaxf(sig_next, 0x1p-100f);
                 const bool full = (w.t + 1) * kTileRows <= L - qlen_b && c0 + C::NC <= qlen_b * p.num_heads;
                 uint32_t seen = 0u;
                 if (!full) seen = (uint32_t)tree_sees(p, b, L, qlen_b, rg, c0 + 16 * cq, 16);
                 more = !w.advance(tile_off, (int)rank, mode, seq_len);
-                sig_next = row_scale(w);  // of the next tile: in flight until the next round
+                const int next_page = page_of(w);  // of the next tile: looked up until the vote
                 ok = ok && spin_phase<false>(bar(C::SF + (k & 1)), (k >> 1) & 1, wc, status);
                 tc_fence_after();
                 float x[16], xl[16];
@@ -579,6 +582,7 @@ __global__ void __launch_bounds__(Wide8::THREADS, 1)
                         for (int n = 0; n < 16; ++n) lpart[n] *= al[n];
                     }
                 }
+                sig_next = read_scale(w, next_page);  // in flight until the next tile
                 // ---- P^T: stored 2^(score + log2 s - m + 4), summed as 2^(score - m)
                 const float inv16 = 0.0625f / sig;
                 const float2 inv2 = make_float2(inv16, inv16), four = make_float2(kPScaleLog2_8, kPScaleLog2_8);
