@@ -857,14 +857,20 @@ __device__ __forceinline__ void duo_body(const DuoMaps &tm, const DecodeParams &
                     alpha_s[tid] = (!(l > 0.f) || m_s[tid] == -INFINITY) ? 0.f : 1.f / l;
                 }
                 named_bar_sync(SMX, NSM);
-                auto store_o = [&](int c, int j, float val) {
-                    const int d = 256 * (int)rank + 128 * j + row;
-                    const int ng = grp * NC + c;
-                    if (ng >= p.ncols) return;
-                    if (nsplit == 1)
-                        p.o[((int64_t)b * p.ncols + ng) * kDv + d] = __float2bfloat16_rn(val);
-                    else
-                        p.opart[((int64_t)slot * p.ncols + ng) * kDv + d] = val;
+                // 16 columns of latent row d: outputs of an unsplit sequence, else partials
+                auto store16 = [&](int c, int d, const float (&v)[16]) {
+                    const int cols = min(p.ncols - (grp * NC + c), 16);
+                    if (nsplit == 1) {
+                        __nv_bfloat16 *o = p.o + ((int64_t)b * p.ncols + grp * NC + c) * kDv + d;
+#pragma unroll
+                        for (int n = 0; n < 16; ++n)
+                            if (n < cols) o[n * kDv] = __float2bfloat16_rn(v[n]);
+                    } else {
+                        float *o = p.opart + ((int64_t)slot * p.ncols + grp * NC + c) * kDv + d;
+#pragma unroll
+                        for (int n = 0; n < 16; ++n)
+                            if (n < cols) o[n * kDv] = v[n];
+                    }
                 };
 #pragma unroll 1
                 for (int j = 0; j < 2; ++j) {
@@ -875,12 +881,13 @@ __device__ __forceinline__ void duo_body(const DuoMaps &tm, const DecodeParams &
                         if constexpr (C::SPLIT)
                             tmem_ld16(tmem + lane_addr + C::O_COL + (uint32_t)j * C::NP + half * 64 + NH + 16 * g, lo);
                         tmem_wait_ld();
+                        const int c = half * NH + 16 * g;
 #pragma unroll
                         for (int n = 0; n < 16; ++n) {
-                            const int c = half * NH + 16 * g + n;
                             const float val = C::SPLIT ? hi[n] + lo[n] : hi[n];
-                            store_o(c, j, val * alpha_s[c]);
+                            hi[n] = val * alpha_s[c + n];
                         }
+                        store16(c, 256 * (int)rank + 128 * j + row, hi);
                     }
                 }
                 if (rank == 0 && tid < NC) {
