@@ -80,9 +80,9 @@ struct DuoCfg {
     static constexpr uint32_t IDESC_S = idesc_bf16_f32(256, NC, 0, 0);
     static constexpr uint32_t IDESC_O = idesc_bf16_f32(256, NP, 1, 1);
 };
-// Ring slots, measured: 64 columns at B=16, q_len*h=64, 32768 rows: 4 K chunks + 2 value pairs 163 us, 3 + 3
-// 170 us, 5 + 2 166 us, and with value slots of half the size 4 + 5 164 us; 128 columns at B=8, h=128,
-// q_len=4: 3 + 2 208 us, 5 + 1 233 us, half-size slots 3 + 4 217 us.
+// Ring slots, measured: 64 columns at B=16, q_len*h=64, 32768 rows: 4 K chunks + 2 value pairs 152 us, 3 + 3
+// 158 us, 5 + 2 154 us (value slots of half the size, 4 + 5: no gain over 4 + 2); 128 columns at B=8,
+// h=128, q_len=4: 5 + 1 slots take 12 % longer than 3 + 2, half-size slots 3 + 4 4 % longer.
 using DuoCfg64 = DuoCfg<64, true, 4, 2>;     // 64 columns, P as bf16 hi + lo
 using DuoCfg128 = DuoCfg<128, false, 3, 2>;  // 128 columns, one bf16 P term
 constexpr uint32_t kDuoSmemAlloc =

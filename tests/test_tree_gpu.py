@@ -220,6 +220,95 @@ def test_same_inputs_same_bits():
         assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
 
 
+@pytest.mark.parametrize("heads,q_len", [(16, 9), (128, 2), (5, 26), (64, 16)])
+def test_long_rows_on_the_e4m3_cache(heads, q_len):
+    """128-column groups, whose two CTAs take 64 columns each; rows scaled x8 move the maxima."""
+    w = W.make_workload(2, heads, [8192, 9001], q_len=q_len, paged=True, seed=13, spike_frac=0.05, kv_dtype="e4m3")
+    check(w, tree_masks(np.random.default_rng(7), 2, q_len), "e4m3 mode 1")
+
+
+@pytest.mark.parametrize("heads,q_len", [(16, 1), (16, 4), (20, 5)])
+def test_e4m3_rows_of_very_unequal_scale(heads, q_len):
+    """Row scales over twelve orders of two, rising and falling along the sequence, and rows of zeros."""
+    lens = [1500, 333, 640]
+    w = W.make_workload(3, heads, lens, q_len=q_len, seed=14, kv_dtype="e4m3")
+    rows = torch.arange(w.kv_scale.shape[1])
+    w.kv_scale *= torch.exp2(6.0 * torch.sin(rows / 70.0)).float()
+    w.kv8[:, 100:130] = 0
+    check(w, tree_masks(np.random.default_rng(8), 3, q_len), "unequal scales")
+
+
+@pytest.mark.parametrize("kv", DTYPES)
+def test_splits_of_a_long_sequence(kv):
+    """One sequence over all SMs, and a neighbour of one tile."""
+    w = W.make_workload(2, 16, [40000, 100], q_len=4, paged=True, seed=15, spike_frac=0.01, kv_dtype=kv)
+    check(w, tree_masks(np.random.default_rng(9), 2, 4), "long split")
+
+
+@pytest.mark.parametrize("heads,q_len,lens,kv", [(16, 4, [6000, 3000, 9000, 500], "e4m3"),
+                                                 (128, 2, [8200, 9000], "e4m3"), (16, 4, [6000, 3000, 700], "bf16"),
+                                                 (4, 4, [6000, 500], "bf16"), (4, 4, [6000, 500], "e4m3")])
+def test_repeated_trees_are_bitwise_identical(heads, q_len, lens, kv):
+    """Stress of the hand-offs between roles and CTAs: 200 plan + decode calls give one result."""
+    w = W.make_workload(len(lens), heads, lens, q_len=q_len, seed=16, kv_dtype=kv, spike_frac=0.02)
+    masks = tree_masks(np.random.default_rng(10), len(lens), q_len)
+    o, lse = check(w, masks, "first of many")
+    dec = m.MlaDecoder(w.batch, q_len, heads, device="cuda")
+    sl, q = w.seqlens.cuda(), w.q.cuda()
+    mask = torch.from_numpy(ref.mask_words(masks, q_len).copy()).cuda()
+    kvs = (w.kv8.cuda(), w.kv_scale.cuda()) if kv == "e4m3" else (w.kv.cuda(),)
+    fwd = dec.fwd_tree_fp8 if kv == "e4m3" else dec.fwd_tree
+    differ = torch.zeros((), dtype=torch.int64, device="cuda")
+    for _ in range(200):
+        dec.plan(sl)
+        o2, lse2 = fwd(q, *kvs, sl, mask)
+        differ += (o2 != o).sum() + (lse2 != lse).sum()
+    assert int(differ) == 0 and dec.status() == 0
+
+
+@pytest.mark.parametrize("heads,q_len,kv", [(4, 4, "bf16"), (16, 4, "bf16"), (4, 4, "e4m3"), (16, 4, "e4m3")])
+def test_bounded_waits_of_the_tree_kernels(heads, q_len, kv):
+    """Q withheld: the waits run out, the status says so, and the next decode on the workspace is right."""
+    w = W.make_workload(2, heads, [700, 300], q_len=q_len, seed=17, kv_dtype=kv)
+    masks = tree_masks(np.random.default_rng(11), 2, q_len)
+    assert run_tree(w, masks, flags=m.FLAG_TEST_EXPIRE_WAITS)[2] == -6
+    check(w, masks, "after a timeout")
+
+
+@pytest.mark.parametrize("heads,kv", [(4, "bf16"), (16, "bf16"), (16, "e4m3")])
+def test_lengths_out_of_range_are_reported(heads, kv):
+    w = W.make_workload(2, heads, [100, 300], q_len=4, seed=18, kv_dtype=kv)
+    masks = tree_masks(np.random.default_rng(12), 2, 4)
+    for q_lens in ([-1, 2], [2, 5]):
+        w.q_lens = torch.tensor(q_lens, dtype=torch.int32)
+        assert run_tree(w, masks)[2] == -1
+    w.q_lens = None
+    w.seqlens = torch.tensor([100, 301], dtype=torch.int32)
+    assert run_tree(w, masks)[2] == -1
+
+
+def test_two_streams_two_workspaces():
+    """Two decodes at once, on streams and workspaces of their own, give what each gives alone."""
+    ws = [W.make_workload(3, 16, [3000, 257, 1536], q_len=4, seed=s, kv_dtype=kv) for s, kv in ((19, "bf16"), (20, "e4m3"))]
+    masks = tree_masks(np.random.default_rng(13), 3, 4)
+    alone = [run_tree(w, masks)[:2] for w in ws]
+    mask = torch.from_numpy(ref.mask_words(masks, 4).copy()).cuda()
+    decs = [m.MlaDecoder(3, 4, 16, device="cuda") for _ in ws]
+    streams = [torch.cuda.Stream() for _ in ws]
+    args = [(w.q.cuda(), *((w.kv8.cuda(), w.kv_scale.cuda()) if w.fp8 else (w.kv.cuda(),)), w.seqlens.cuda(), mask)
+            for w in ws]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        outs = []
+        for w, dec, s, a in zip(ws, decs, streams, args):
+            dec.plan(a[-2], stream=s)
+            with torch.cuda.stream(s):
+                outs.append((dec.fwd_tree_fp8 if w.fp8 else dec.fwd_tree)(*a, stream=s))
+        torch.cuda.synchronize()
+        for (o, lse), (o2, lse2) in zip(alone, outs):
+            assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
 # ------------------------------------------------------------------------------------ the whole step
 @pytest.mark.parametrize("kv,heads,captured", [("bf16", 16, False), ("e4m3", 16, False), ("bf16", 4, True),
                                                ("e4m3", 16, True)])
