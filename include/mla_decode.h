@@ -91,7 +91,7 @@ MLA_API size_t mla_decode_workspace_size(int batch, int q_len, int num_heads, in
  * Split-KV scheduling metadata (not on the pages: needed so that a batch with
  * few sequences still fills every SM). Reads seqlens (device int32[batch]),
  * concatenates the KV units of all sequences (128 rows each for the CTA-pair
- * kernel, 256 for the M = 256 kernel), cuts them into one contiguous range per
+ * kernel, 256 for the M = 256 kernel and the tree decodes), cuts them into one contiguous range per
  * work unit and column group, balanced by cost (each sequence end counts as the
  * units its epilogue and merge take, so a range may be empty), and records for
  * each sequence how many ranges touch it and where its partial results go. One
@@ -398,7 +398,9 @@ MLA_API int mla_decode_read_status(const void *workspace, int *status_out, void 
  * is the one mla_decode_fwd uses: for q_len*h > 16, 256-row units (one 128-row tile per CTA of
  * a pair) and column groups of 64, or of 128 when q_len*h > 64 and every nonempty sequence
  * holds at least 8192 rows (the plan picks this on the device from the same lengths); for
- * q_len*h <= 16 it is schedule 0. Writes, when the pointers are non-NULL:
+ * q_len*h <= 16 it is schedule 0. `schedule` 2 is the one the tree decodes use: schedule 1, but for
+ * q_len*h > 64 with groups of 128 also when the batch has at least one 256-row unit for every work
+ * unit of that grouping (mla_decode_fwd_tree_fp8 with q_len*h <= 16 uses schedule 0). Writes, when the pointers are non-NULL:
  *   cta_ranges  int32[num_ctas*2]  flattened unit range [begin, end) of each work unit (cut by
  *                                  cost as mla_decode_plan does; possibly empty)
  *   seq_info    int32[batch*4]     per sequence: unit count, first work unit, number of splits, partial slot offset

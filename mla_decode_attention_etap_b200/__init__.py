@@ -631,7 +631,8 @@ def mla_decode_read_status(workspace, stream=None) -> int:
 
 def mla_decode_plan_host(seqlens, q_len: int, num_heads: int, n_sms: int, schedule: int = 1):
     """Host mirror of a schedule -> (cta_ranges [ctas, 2], seq_info [B, 4], num_ctas, num_groups, unit_rows,
-    group_cols).  schedule 1: the one mla_decode_fwd (bf16 cache) uses; 0: the one mla_decode_fwd_fp8 uses."""
+    group_cols).  schedule 1: the one mla_decode_fwd (bf16 cache) uses; 0: the one mla_decode_fwd_fp8 uses;
+    2: the one the tree decodes use."""
     import numpy as np
     sl = np.ascontiguousarray(np.asarray(seqlens, dtype=np.int32))
     nct, ngr, urows, gcols = ctypes.c_int(0), ctypes.c_int(0), ctypes.c_int(0), ctypes.c_int(0)

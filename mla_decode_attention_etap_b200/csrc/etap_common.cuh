@@ -62,7 +62,8 @@ struct DecodeParams {
     float scale_log2;  // softmax_scale * log2(e)
     unsigned long long wait_limit_ns;
     int withhold_q;    // test hook: never load Q, so that the bounded waits expire
-    int cta_ranges_off, tile_off_off, seq_info_off, cta_seq_off;  // int32 offsets into ws
+    int64_t cta_ranges_off, tile_off_off, seq_info_off, cta_seq_off;  // int32 offsets into ws
+    int sched_hdr, sched_id;  // header words of the schedule, and what kHdrSchedUsed says of it (duo or tree)
     int32_t *counters;  // [batch][groups][2]: split CTAs done per (sequence, column group, rank)
     int slots;          // partial slots (stride between the two ranks' LSE partial arrays)
     int fuse_merge;     // the last split CTA of a sequence merges the partials (no combine launch)

@@ -36,6 +36,8 @@
 // Every wait is bounded; see etap_common.cuh.
 #pragma once
 
+#include <type_traits>
+
 #include "etap_common.cuh"
 
 namespace mla {
@@ -209,6 +211,16 @@ __device__ __forceinline__ void duo_body(const DuoMaps &tm, const DecodeParams &
         return L < 0 ? 0 : L;
     };
 
+    // Passes of step 3 over a unit of sequence b.  In 128-column groups the tree schedule also holds
+    // sequences for which one bf16 P term is not accurate enough: their units are multiplied twice, by
+    // P_hi and then by what its rounding left (the value columns are loaded again, from L2).
+    auto passes_of = [&](int L) -> int {
+        if constexpr (TREE && !C::SPLIT)
+            return L < kSingleP_MinRows ? 2 : 1;
+        else
+            return 1;
+    };
+
     if (warp == 0) {
         // ------------------------------------------------------------ K tiles and Q (step-1 operands)
         // The loops of warps 0, 1, 2 and 11 are run by the whole warp; one lane issues (see elect_one).
@@ -295,6 +307,7 @@ __device__ __forceinline__ void duo_body(const DuoMaps &tm, const DecodeParams &
         look_up();
         while (__all_sync(0xffffffffu, ok && w.valid)) {
             int ya[2], yb[2], valid[2];
+            const int passes = __shfl_sync(0xffffffffu, passes_of(L), 0);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 ya[h] = __shfl_sync(0xffffffffu, loaded[h][0] ? y[h][0] : -1, 0);
@@ -303,6 +316,8 @@ __device__ __forceinline__ void duo_body(const DuoMaps &tm, const DecodeParams &
             }
             w.advance(tile_off);
             look_up();  // of the next unit, while this one's slots come free
+#pragma unroll 1
+            for (int pass = 0; pass < passes && ok; ++pass)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
 #pragma unroll 1
@@ -443,10 +458,11 @@ __device__ __forceinline__ void duo_body(const DuoMaps &tm, const DecodeParams &
                 TraceRowT<TR> tr;
                 tr.init(p, 4);
                 if (!lead) tr.row = nullptr;
+                int pass = 0;  // kp counts passes
                 while (__all_sync(0xffffffffu, ok && pc.valid)) {
-                    if (lead) mbar_arrive_expect_tx(bar(BR::XF), C::P_BUF);  // the odd CTA's part of unit kp
+                    if (lead) mbar_arrive_expect_tx(bar(BR::XF), C::P_BUF);  // the odd CTA's part of pass kp
                     __syncwarp();
-                    const uint32_t fresh = __any_sync(0xffffffffu, pc.first()) ? 0u : 1u;
+                    const uint32_t fresh = __any_sync(0xffffffffu, pc.first() && pass == 0) ? 0u : 1u;
 #pragma unroll 1
                     for (uint32_t h = 0; h < 2; ++h) {
                         ok = poll_phase_cluster(bar(h == 0 ? BR::PF0 : BR::PF1), kp & 1, wc, status);
@@ -481,8 +497,11 @@ __device__ __forceinline__ void duo_body(const DuoMaps &tm, const DecodeParams &
                         __syncwarp();
                     }
                     tr.put(kEvS3Done, kp);
-                    pc.advance(tile_off);
                     ++kp;
+                    if (++pass == passes_of(seq_len(pc.b))) {
+                        pc.advance(tile_off);
+                        pass = 0;
+                    }
                 }
                 pv_pending = lead;  // FINAL3 is committed (and drained) at the end of the kernel
             }
@@ -493,7 +512,7 @@ __device__ __forceinline__ void duo_body(const DuoMaps &tm, const DecodeParams &
             TileCursor rc;
             rc.init(tile_off, seq0, fb, fe);
             const uint32_t pf0_remote = map_to_rank(bar(BR::PF0), 0);
-            int kr = 0;
+            int kr = 0, pass = 0;  // kr counts passes
             bool ok = true;
             while (rc.valid && ok) {
                 mbar_arrive_expect_tx(bar(BR::XF), C::P_BUF);
@@ -515,8 +534,11 @@ __device__ __forceinline__ void duo_body(const DuoMaps &tm, const DecodeParams &
                 fence_acquire_cluster_smem();
                 fence_proxy_async_smem();  // the st.async writes are read by the tensor core next
                 mbar_arrive_remote(pf0_remote);
-                rc.advance(tile_off);
                 ++kr;
+                if (++pass == passes_of(seq_len(rc.b))) {
+                    rc.advance(tile_off);
+                    pass = 0;
+                }
             }
         }
         __syncwarp();
@@ -552,7 +574,7 @@ __device__ __forceinline__ void duo_body(const DuoMaps &tm, const DecodeParams &
         const uint32_t mx_remote = map_to_rank(sbase + kDuoCtlMx, peer);
         const uint32_t lx_remote = map_to_rank(sbase + kDuoCtlLx, peer);
         bool ok = true, stop = false;
-        int k = 0, xmr = 0, xlr = 0;
+        int k = 0, kv = 0, xmr = 0, xlr = 0;  // units, passes of step 3, exchange rounds
         TraceRowT<TR> tr;
         tr.init(p, 3);
         if (tid != 0) tr.row = nullptr;
@@ -589,7 +611,8 @@ __device__ __forceinline__ void duo_body(const DuoMaps &tm, const DecodeParams &
         // CTA's buffer (own columns) or the peer's (st.async, counted on its XF barrier); the
         // probabilities are added to lpart.
         float lpart[NH];
-        auto write_p = [&](bool full, int rg) {
+        // (rest: the term that P_hi's rounding left, for a second pass of step 3)
+        auto write_p = [&](bool full, int rg, auto rest) {
 #pragma unroll
             for (int cc = 0; cc < NH / 32; ++cc) {
                 float x[32];
@@ -608,16 +631,18 @@ __device__ __forceinline__ void duo_body(const DuoMaps &tm, const DecodeParams &
                             const float2 d = add2(make_float2(x[n], x[n + 1]),
                                                   e == 0 ? make_float2(nm.x, nm.y) : make_float2(nm.z, nm.w));
                             const float2 pv = make_float2(fast_exp2(d.x), fast_exp2(d.y));
-                            const float2 l = add2(make_float2(lpart[32 * cc + n], lpart[32 * cc + n + 1]), pv);
-                            lpart[32 * cc + n] = l.x;
-                            lpart[32 * cc + n + 1] = l.y;
                             const uint32_t h = pack_bf16x2(pv.x, pv.y);
-                            hi[2 * q + e / 2] = h;
-                            if constexpr (C::SPLIT) {
+                            if constexpr (!decltype(rest)::value) {
+                                const float2 l = add2(make_float2(lpart[32 * cc + n], lpart[32 * cc + n + 1]), pv);
+                                lpart[32 * cc + n] = l.x;
+                                lpart[32 * cc + n + 1] = l.y;
+                                hi[2 * q + e / 2] = h;
+                            }
+                            if constexpr (C::SPLIT || decltype(rest)::value) {
                                 // p - hi, exactly rounded as a subtraction
                                 const float2 r = fma2(make_float2(__uint_as_float(h << 16), __uint_as_float(h & 0xFFFF0000u)),
                                                       make_float2(-1.f, -1.f), pv);
-                                lo[2 * q + e / 2] = pack_bf16x2(r.x, r.y);
+                                (C::SPLIT ? lo : hi)[2 * q + e / 2] = pack_bf16x2(r.x, r.y);
                             }
                         }
                     }
@@ -643,6 +668,7 @@ __device__ __forceinline__ void duo_body(const DuoMaps &tm, const DecodeParams &
                 int L = p.seqlens[b];
                 if ((int64_t)L > l_cap) L = (int)l_cap;
                 if (L < 0) L = 0;
+                const int passes = passes_of(L);
                 const int seg_nsplit = seq_info[4 * b + 2];
                 const int seg_slot = seq_info[4 * b + 3] + (unit - seq_info[4 * b + 1]);
                 int qlen_b = p.q_len;
@@ -770,9 +796,9 @@ __device__ __forceinline__ void duo_body(const DuoMaps &tm, const DecodeParams &
                         if (any_resc) {
                             // O^T holds step 3 up to the previous unit once both of its K-halves completed;
                             // rescale this thread's lane of both M-blocks for its half's columns
-                            if (k > 0) {
-                                ok = ok && spin_phase<false>(bar(BR::PE0), (k - 1) & 1, wc, status);
-                                ok = ok && spin_phase<false>(bar(BR::PE1), (k - 1) & 1, wc, status);
+                            if (kv > 0) {
+                                ok = ok && spin_phase<false>(bar(BR::PE0), (kv - 1) & 1, wc, status);
+                                ok = ok && spin_phase<false>(bar(BR::PE1), (kv - 1) & 1, wc, status);
                             }
                             tc_fence_after();
 #pragma unroll
@@ -793,33 +819,43 @@ __device__ __forceinline__ void duo_body(const DuoMaps &tm, const DecodeParams &
                             for (int n = 0; n < NH; ++n) lpart[n] *= alpha_s[half * NH + n];
                         }
                     }
-                    // ---- P^T of this CTA's rows (K-half `rank`) once step 3 of the previous unit released that
+                    // ---- P^T of this CTA's rows (K-half `rank`) once the previous pass of step 3 released that
                     // K-half's buffers in both CTAs
-                    if (k > 0)
-                        ok = ok && spin_phase<false>(bar(rank == 0 ? BR::PE0 : BR::PE1), (k - 1) & 1, wc, status);
-                    tc_fence_after();
-                    tr.put(kEvSmPe, k);
-                    write_p(full, rg);
-                    // this CTA's P^T writes are seen by the tensor core's reads; the S^T reads are complete
-                    fence_proxy_async_smem();
-                    tc_fence_before();
-                    if (!named_bar_and(SMX, NSM, ok)) {
-                        stop = true;
-                        break;
-                    }
-                    if (tid == 0) {
-                        // K-half `rank` is ready on this side (the receiving side reports its part)
-                        if (leader)
-                            mbar_arrive(bar(BR::PF0));
-                        else
-                            mbar_arrive_remote(map_to_rank(bar(BR::PF1), 0));
-                        arrive0(BR::SE + (k & 1));
-                        tr.put(kEvSmDone, k);
+#pragma unroll 1
+                    for (int pass = 0; pass < passes; ++pass, ++kv) {
+                        if (kv > 0)
+                            ok = ok && spin_phase<false>(bar(rank == 0 ? BR::PE0 : BR::PE1), (kv - 1) & 1, wc, status);
+                        tc_fence_after();
+                        tr.put(kEvSmPe, k);
+                        if constexpr (TREE && !C::SPLIT) {
+                            if (pass == 0)
+                                write_p(full, rg, std::false_type{});
+                            else
+                                write_p(full, rg, std::true_type{});
+                        } else {
+                            write_p(full, rg, std::false_type{});
+                        }
+                        // this CTA's P^T writes are seen by the tensor core's reads; the S^T reads are complete
+                        fence_proxy_async_smem();
+                        tc_fence_before();
+                        if (!named_bar_and(SMX, NSM, ok)) {
+                            stop = true;
+                            break;
+                        }
+                        if (tid == 0) {
+                            // K-half `rank` is ready on this side (the receiving side reports its part)
+                            if (leader)
+                                mbar_arrive(bar(BR::PF0));
+                            else
+                                mbar_arrive_remote(map_to_rank(bar(BR::PF1), 0));
+                            if (pass == passes - 1) arrive0(BR::SE + (k & 1));
+                            tr.put(kEvSmDone, k);
+                        }
                     }
                 }
                 if (stop) break;
                 // ---------------------------------------------------- epilogue for this CTA's 256 latent rows
-                const int kl = k - 1;  // the segment's last unit: its step 3 has completed
+                const int kl = kv - 1;  // the segment's last pass: its step 3 has completed
                 tr.put(kEvSmEpi, kl);
                 ok = ok && spin_phase<false>(bar(BR::PE0), kl & 1, wc, status);
                 ok = ok && spin_phase<false>(bar(BR::PE1), kl & 1, wc, status);
@@ -988,14 +1024,14 @@ __global__ void __launch_bounds__(kDuoThreads, 1)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     // The schedule must come from a plan for this same shape (uniform in the whole cluster).
-    const int mode = p.ws[kHdrDuo + kSchMode];
-    const int groups = p.ws[kHdrDuo + kSchGroups];
-    const int ctas = p.ws[kHdrDuo + kSchCtas];
+    const int mode = p.ws[p.sched_hdr + kSchMode];
+    const int groups = p.ws[p.sched_hdr + kSchGroups];
+    const int ctas = p.ws[p.sched_hdr + kSchCtas];
     const bool plan_ok = p.ws[kHdrBatch] == p.batch && p.ws[kHdrCols] == p.ncols && (mode == 0 || mode == 1) &&
-                         p.ws[kHdrDuo + kSchGroupCols] == duo_group_cols(mode) &&
+                         p.ws[p.sched_hdr + kSchGroupCols] == duo_group_cols(mode) &&
                          groups == duo_groups(p.ncols, mode) && ctas >= 1 && ctas * groups <= (int)(gridDim.x >> 1);
     if (!plan_ok && threadIdx.x == 0) atomicCAS(status, 0, kStatusInvalid);
-    if (blockIdx.x == 0 && threadIdx.x == 0) p.ws[kHdrSchedUsed] = 1;  // the partials follow the duo schedule
+    if (blockIdx.x == 0 && threadIdx.x == 0) p.ws[kHdrSchedUsed] = p.sched_id;  // the partials' schedule
     const int cluster = (int)(blockIdx.x >> 1);
     const int unit = plan_ok ? cluster / groups : 0;
     const int grp = plan_ok ? cluster % groups : 0;

@@ -2,7 +2,7 @@
 // columns.
 //
 // Computation as in etap_pair_kernel.cuh's E4M3 configurations: S^T = K Q^T with Q as two E4M3 terms
-// times a power of two per column, P^T as two E4M3 terms of 2^(score + log2 s - m + 4) (s: the row's
+// times a power of two per column, P^T as two E4M3 terms of 2^(score + log2 s - m + PSCALE) (s: the row's
 // scale), O^T = V^T P^T, fp32 accumulation.  What differs is the layout, made for 64 columns:
 //
 //   * A CTA holds whole 128-row tiles (72 KB of codes) and all of its 64 columns' Q (72 KB: [Q_hi; Q_lo]
@@ -13,7 +13,7 @@
 //     M-tiles of 64 columns leave the TMEM room for two score buffers of 128.
 //   * Sixteen softmax warps, four per TMEM lane quadrant: a thread holds one row and 16 columns, and
 //     its row's scale is read a tile ahead.
-//   * It runs on the M = 256 schedule (256-row units, one range per 2-CTA cluster).  In its 64-column
+//   * It runs on the M = 256 kernel's schedules (256-row units, one range per 2-CTA cluster).  In its 64-column
 //     groups the two CTAs take the two tiles of a unit and merge their results once per segment through
 //     distributed shared memory; in its 128-column groups each takes 64 of the columns and both tiles,
 //     and nothing is merged.
@@ -31,6 +31,13 @@ struct Wide8 {
     static constexpr int NC = 64;                      // query columns of a CTA
     static constexpr int NV = 8;                       // 16 KB slots: 128 rows x 128 codes
     static constexpr int THREADS = 640, NSM = 512;     // softmax threads: warps 4..19
+    // P^T is stored times 2^PSCALE.  m is set HEADROOM above a tile's maximum and moves once a row exceeds it
+    // by THRESH, so that a stored p is at most 2^(THRESH + PSCALE) = 256 (E4M3 ends at 448) and the largest of
+    // a column, right after m moved, is 2^(PSCALE - HEADROOM) = 16.  The low term resolves 2^-10, 2^-14 of
+    // that: the rows around a sequence's typical score, some 2^-5 of its largest, keep the 8 bits of two
+    // E4M3 terms.  (With 4, 2 and 4 in their places, 2^-12: the error of O over 3000 rows was 2.0e-3 of its
+    // RMS, bf16's rounding of O alone being 1.65e-3.)
+    static constexpr float PSCALE = 5.f, PUNIT = 0.03125f, THRESH = 3.f, HEADROOM = 1.f;
     static constexpr uint32_t CHUNK = 16384, HALF = 8192;
     static constexpr uint32_t R_ROW = 64, R_DATA = 128 * R_ROW, R_HALF = 64 * R_ROW;
     static constexpr uint32_t Q_CHUNK = 2 * NC * 128, P_TERM = 128 * NC;
@@ -41,7 +48,7 @@ struct Wide8 {
     static constexpr uint32_t OFF_P = OFF_QR + 2 * NC * R_ROW;  // P_hi, then P_lo
     static constexpr uint32_t OFF_BAR = OFF_P + 2 * P_TERM;
     static constexpr uint32_t OFF_MISC = OFF_BAR + 256;  // +0 TMEM address, +16 WaitCtl
-    static constexpr uint32_t OFF_M = OFF_MISC + 64;     // float[64] minus the running maximum (log2 units)
+    static constexpr uint32_t OFF_M = OFF_MISC + 64;     // float[64] PSCALE minus the running maximum m (log2 units)
     static constexpr uint32_t OFF_ALPHA = OFF_M + 256;   // float[64] rescale factors; the epilogue's factors of this CTA's part
     static constexpr uint32_t OFF_QV = OFF_ALPHA + 256;  // float[64] 2^-c; the epilogue's of the peer's
     static constexpr uint32_t BYTES = OFF_QV + 256;
@@ -138,14 +145,14 @@ __global__ void __launch_bounds__(Wide8::THREADS, 1)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     // The schedule must come from a plan for this same shape (uniform in the whole cluster).
-    const int mode = p.ws[kHdrDuo + kSchMode];
-    const int groups = p.ws[kHdrDuo + kSchGroups];
-    const int ctas = p.ws[kHdrDuo + kSchCtas];
+    const int mode = p.ws[p.sched_hdr + kSchMode];
+    const int groups = p.ws[p.sched_hdr + kSchGroups];
+    const int ctas = p.ws[p.sched_hdr + kSchCtas];
     const bool plan_ok = p.ws[kHdrBatch] == p.batch && p.ws[kHdrCols] == p.ncols && (mode == 0 || mode == 1) &&
-                         p.ws[kHdrDuo + kSchGroupCols] == duo_group_cols(mode) &&
+                         p.ws[p.sched_hdr + kSchGroupCols] == duo_group_cols(mode) &&
                          groups == duo_groups(p.ncols, mode) && ctas >= 1 && ctas * groups <= (int)(gridDim.x >> 1);
     if (!plan_ok && threadIdx.x == 0) atomicCAS(status, 0, kStatusInvalid);
-    if (blockIdx.x == 0 && threadIdx.x == 0) p.ws[kHdrSchedUsed] = 1;  // the partials follow the duo schedule
+    if (blockIdx.x == 0 && threadIdx.x == 0) p.ws[kHdrSchedUsed] = p.sched_id;  // the partials' schedule
     const int cluster = (int)(blockIdx.x >> 1);
     const int unit = plan_ok ? cluster / groups : 0;
     const int grp = plan_ok ? cluster % groups : 0;
@@ -517,7 +524,7 @@ __global__ void __launch_bounds__(Wide8::THREADS, 1)
                 // x = score + log2 s; does any pass its column's maximum?
                 const float lgs = __log2f(sig);
                 const float2 sig2 = make_float2(sig, sig), lgs2 = make_float2(lgs, lgs);
-                const float4 *m4 = reinterpret_cast<const float4 *>(m_s + 16 * cq);  // -m per column
+                const float4 *m4 = reinterpret_cast<const float4 *>(m_s + 16 * cq);  // PSCALE - m per column
                 float over = -INFINITY;
 #pragma unroll
                 for (int n = 0; n < 16; n += 2) {
@@ -538,7 +545,7 @@ __global__ void __launch_bounds__(Wide8::THREADS, 1)
                     const float2 d1 = add2(make_float2(x[4 * q + 2], x[4 * q + 3]), make_float2(mm.z, mm.w));
                     over = fmaxf(over, fmaxf(fmaxf(d0.x, d0.y), fmaxf(d1.x, d1.y)));
                 }
-                const bool need = first || !ok || over > kRescaleThreshold8;
+                const bool need = first || !ok || over > C::THRESH + C::PSCALE;
                 if (named_bar_or(SMX, NSM, need)) {
                     // ---- some score passes its column's maximum: the tile's maxima, new maxima, O^T rescaled.
                     // Step 3 of the last tile completes first (the reduction borrows the P^T buffers).
@@ -555,12 +562,12 @@ __global__ void __launch_bounds__(Wide8::THREADS, 1)
                     if (tid < C::NC) {
                         const float mt = fmaxf(fmaxf(red[tid], red[C::NC + tid]),
                                                fmaxf(red[2 * C::NC + tid], red[3 * C::NC + tid]));
-                        const float mo = -m_s[tid];
+                        const float mo = C::PSCALE - m_s[tid];
                         float a = 1.f;
-                        if (mt > mo + kRescaleThreshold8) {
-                            const float mn = mt + kRescaleHeadroom8;
+                        if (mt > mo + C::THRESH) {
+                            const float mn = mt + C::HEADROOM;
                             a = fast_exp2(mo - mn);  // 0 for a column that saw no row so far
-                            m_s[tid] = -mn;
+                            m_s[tid] = C::PSCALE - mn;
                             resc = !first;  // (a first tile's O^T does not exist yet)
                         }
                         alpha_s[tid] = a;
@@ -583,9 +590,9 @@ __global__ void __launch_bounds__(Wide8::THREADS, 1)
                     }
                 }
                 sig_next = read_scale(w, next_page);  // in flight until the next tile
-                // ---- P^T: stored 2^(score + log2 s - m + 4), summed as 2^(score - m)
-                const float inv16 = 0.0625f / sig;
-                const float2 inv2 = make_float2(inv16, inv16), four = make_float2(kPScaleLog2_8, kPScaleLog2_8);
+                // ---- P^T: stored 2^(score + log2 s - m + PSCALE), summed as 2^(score - m)
+                const float inv = C::PUNIT / sig;
+                const float2 inv2 = make_float2(inv, inv);
                 uint32_t hi[4], lo[4];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
@@ -595,7 +602,7 @@ __global__ void __launch_bounds__(Wide8::THREADS, 1)
                     for (int e = 0; e < 2; ++e) {
                         const int n = 4 * q + 2 * e;
                         const float2 nm = e == 0 ? make_float2(mm.x, mm.y) : make_float2(mm.z, mm.w);
-                        const float2 d = add2(add2(make_float2(x[n], x[n + 1]), nm), four);
+                        const float2 d = add2(make_float2(x[n], x[n + 1]), nm);
                         const float2 pv = make_float2(fast_exp2(d.x), fast_exp2(d.y));
                         const float2 sum = fma2(pv, inv2, make_float2(lpart[n], lpart[n + 1]));
                         lpart[n] = sum.x;
@@ -631,13 +638,13 @@ __global__ void __launch_bounds__(Wide8::THREADS, 1)
             }
             named_bar_sync(SMX, NSM);
             // one thread per column: its sum, (mode 0) both CTAs' parts merged by the log-sum-exp rule, its LSE
-            // and the factors of the two parts in the output, P^T's 2^4 included
+            // and the factors of the two parts in the output, P^T's 2^PSCALE included
             float l_own = 0.f;
             if (tid < C::NC)
                 l_own = (red[tid] + red[C::NC + tid]) + (red[2 * C::NC + tid] + red[3 * C::NC + tid]);
             auto finish_column = [&](float mm, float l, float as, float ap) {
                 const bool empty = !(l > 0.f);
-                const float inv = empty ? 0.f : 0.0625f / l;
+                const float inv = empty ? 0.f : C::PUNIT / l;
                 alpha_s[tid] = as * inv;
                 qv_s[tid] = ap * inv;
                 if (c0 + tid < p.ncols && (mode == 1 || rank == 0)) {
@@ -666,7 +673,7 @@ __global__ void __launch_bounds__(Wide8::THREADS, 1)
             const float4 *fa = reinterpret_cast<const float4 *>(alpha_s + 16 * cq);
             const float4 *fb = reinterpret_cast<const float4 *>(qv_s + 16 * cq);
             if (mode == 1) {
-                if (tid < C::NC) finish_column(-m_s[tid], l_own, 1.f, 0.f);
+                if (tid < C::NC) finish_column(C::PSCALE - m_s[tid], l_own, 1.f, 0.f);
                 named_bar_sync(SMX, NSM);
 #pragma unroll 1
                 for (int i = 0; i < 4; ++i) {
@@ -711,7 +718,7 @@ __global__ void __launch_bounds__(Wide8::THREADS, 1)
                 const float4 *xs = reinterpret_cast<const float4 *>(smem + C::OFF_XM);
                 const float *ml = reinterpret_cast<const float *>(smem + C::OFF_XML);
                 if (tid < C::NC) {
-                    const float m = -m_s[tid], mp = -ml[tid], lp = ml[C::NC + tid];
+                    const float m = C::PSCALE - m_s[tid], mp = C::PSCALE - ml[tid], lp = ml[C::NC + tid];
                     const float mm = fmaxf(m, mp);
                     const float as = fast_exp2(m - mm), ap = fast_exp2(mp - mm);  // 0 for a part without rows
                     // rank 0's term first in both CTAs, so that both compute the same l

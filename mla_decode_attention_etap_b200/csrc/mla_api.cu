@@ -219,9 +219,9 @@ cudaError_t launch_wide8(const CUtensorMap &tm_kv, const CUtensorMap &tm_kvr, co
 }
 
 // The combine kernel, launched as a programmatic dependent of what precedes it on the stream:
-// with spin = 0 it waits for that whole grid; with spin = 1 (after the duo kernel only) its CTAs
-// wait for their own sequence's split counters.
-int launch_combine(void *workspace, int batch, int q_len, int num_heads, int num_sms, void *o, float *lse, int spin,
+// with sched = 0 it waits for that whole grid; with sched = 1 or 2 (after a kernel on the duo or tree
+// schedule only) its CTAs wait for their own sequence's split counters.
+int launch_combine(void *workspace, int batch, int q_len, int num_heads, int num_sms, void *o, float *lse, int sched,
                    unsigned long long wait_limit_ns, cudaStream_t s) {
     const mla::WsLayout lay = mla::ws_layout(batch, q_len, num_heads, num_sms);
     const int ncols = q_len * num_heads;
@@ -239,7 +239,7 @@ int launch_combine(void *workspace, int batch, int q_len, int num_heads, int num
     cudaError_t e = cudaLaunchKernelEx(&cfg, mla::combine_kernel, reinterpret_cast<int32_t *>(ws),
                                        reinterpret_cast<const float *>(ws + lay.opart),
                                        reinterpret_cast<const float *>(ws + lay.lsepart), ncols, lay,
-                                       reinterpret_cast<__nv_bfloat16 *>(o), lse, spin, wait_limit_ns);
+                                       reinterpret_cast<__nv_bfloat16 *>(o), lse, sched, wait_limit_ns);
     if (e != cudaSuccess) return cuda_fail(e, "combine_kernel launch");
     e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e, "combine_kernel launch");
@@ -277,17 +277,21 @@ int mla_decode_plan_host(const int32_t *seqlens, int batch, int q_len, int num_h
                          int *unit_rows_out, int *group_cols_out) {
     int st = check_shape(batch, q_len, num_heads, num_sms);
     if (st != MLA_OK) return st;
-    if (!seqlens || (schedule != 0 && schedule != 1)) return MLA_ERR_INVALID_ARG;
+    if (!seqlens || schedule < 0 || schedule > 2) return MLA_ERR_INVALID_ARG;
     const mla::WsLayout lay = mla::ws_layout(batch, q_len, num_heads, num_sms);
     const int ncols = q_len * num_heads;
-    // schedule 1 (the bf16 cache) is the duo schedule when the shape has one, else the pair schedule
-    const bool duo = schedule == 1 && lay.has_duo;
+    // schedule 1 (the bf16 cache) is the duo schedule when the shape has one, else the pair schedule;
+    // schedule 2 (tree decodes) the tree schedule when it has one, else that of schedule 1
+    const bool duo = schedule >= 1 && lay.has_duo;
     int ctas = lay.ctas, groups = lay.groups, unit_rows = mla::kTileRows, gcols = mla::group_cols(ncols);
     if (duo) {
         int mn = 0;
         for (int b = 0; b < batch; ++b)
             if (seqlens[b] > 0 && (mn == 0 || seqlens[b] < mn)) mn = seqlens[b];
-        const int mode = mla::duo_mode(ncols, mn);
+        int64_t units = 0;
+        for (int b = 0; b < batch; ++b) units += mla::units_of(seqlens[b], mla::kDuoRows);
+        const int mode = schedule == 2 && lay.has_tree ? mla::tree_mode(ncols, mn, units, num_sms)
+                                                       : mla::duo_mode(ncols, mn);
         groups = mla::duo_groups(ncols, mode);
         ctas = mla::num_ctas(num_sms, groups);
         unit_rows = mla::kDuoRows;
@@ -348,12 +352,13 @@ int mla_decode_plan(const int32_t *seqlens, int batch, int q_len, int num_heads,
     if (!seqlens || !workspace) return MLA_ERR_INVALID_ARG;
     if (!aligned(seqlens, 4) || !aligned(workspace, 256)) return MLA_ERR_ALIGNMENT;
     const mla::WsLayout lay = mla::ws_layout(batch, q_len, num_heads, num_sms);
-    if (workspace_bytes < lay.total) return MLA_ERR_WORKSPACE;
+    if (workspace_bytes < lay.base) return MLA_ERR_WORKSPACE;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     // Programmatic dependent launch: the plan is scheduled while the preceding kernel drains
     // and waits for it to complete before its first global read.
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(lay.has_duo ? 2 : 1, 1, 1);  // a CTA per schedule
+    // a CTA per schedule (the tree schedule where the workspace has room for it)
+    cfg.gridDim = dim3(1 + lay.has_duo + (lay.has_tree && workspace_bytes >= lay.total ? 1 : 0), 1, 1);
     cfg.blockDim = dim3(mla::kPlanThreads, 1, 1);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
@@ -420,7 +425,7 @@ int decode_fwd_impl(const void *q, const void *kv, const float *kv_scale, const 
         !aligned(workspace, 256) || !aligned(q_lens, 4) || !aligned(kv_scale, 4) || !aligned(tree_mask, 4))
         return MLA_ERR_ALIGNMENT;
     const mla::WsLayout lay = mla::ws_layout(batch, q_len, num_heads, num_sms);
-    if (workspace_bytes < lay.total) return MLA_ERR_WORKSPACE;
+    if (workspace_bytes < (tree_mask ? lay.total : lay.base)) return MLA_ERR_WORKSPACE;
     const int ncols = q_len * num_heads;
 
     st = ensure_smem_attr();
@@ -480,10 +485,10 @@ int decode_fwd_impl(const void *q, const void *kv, const float *kv_scale, const 
     p.scale_log2 = softmax_scale * 1.4426950408889634f;
     p.wait_limit_ns = (flags & MLA_FLAG_TEST_EXPIRE_WAITS) ? mla::kTestWaitLimitNs : mla::kWaitLimitNs;
     p.withhold_q = (flags & MLA_FLAG_TEST_EXPIRE_WAITS) ? 1 : 0;
-    p.cta_ranges_off = (int)(lay.pair.cta_ranges / 4);
-    p.tile_off_off = (int)(lay.pair.tile_off / 4);
-    p.seq_info_off = (int)(lay.pair.seq_info / 4);
-    p.cta_seq_off = (int)(lay.pair.cta_seq / 4);
+    p.cta_ranges_off = (int64_t)(lay.pair.cta_ranges / 4);
+    p.tile_off_off = (int64_t)(lay.pair.tile_off / 4);
+    p.seq_info_off = (int64_t)(lay.pair.seq_info / 4);
+    p.cta_seq_off = (int64_t)(lay.pair.cta_seq / 4);
     p.counters = reinterpret_cast<int32_t *>(ws + lay.pair.counters);
     p.slots = lay.slots;
     p.trace = trace;
@@ -543,13 +548,17 @@ int decode_fwd_impl(const void *q, const void *kv, const float *kv_scale, const 
             if (st != MLA_OK) return st;
         }
         // the plan picks the grouping on the device (see plan_core.h); the kernel reads it from the header
-        p.ctas = lay.duo.ctas_max;
-        p.groups = lay.duo.groups_max;
-        p.cta_ranges_off = (int)(lay.duo.cta_ranges / 4);
-        p.tile_off_off = (int)(lay.duo.tile_off / 4);
-        p.seq_info_off = (int)(lay.duo.seq_info / 4);
-        p.cta_seq_off = (int)(lay.duo.cta_seq / 4);
-        p.counters = reinterpret_cast<int32_t *>(ws + lay.duo.counters);
+        const bool tree = tree_mask && lay.has_tree;
+        const mla::Sched &sc = tree ? lay.tree : lay.duo;
+        p.sched_hdr = tree ? mla::kHdrTree : mla::kHdrDuo;
+        p.sched_id = tree ? 2 : 1;
+        p.ctas = sc.ctas_max;
+        p.groups = sc.groups_max;
+        p.cta_ranges_off = (int64_t)(sc.cta_ranges / 4);
+        p.tile_off_off = (int64_t)(sc.tile_off / 4);
+        p.seq_info_off = (int64_t)(sc.seq_info / 4);
+        p.cta_seq_off = (int64_t)(sc.cta_seq / 4);
+        p.counters = reinterpret_cast<int32_t *>(ws + sc.counters);
         // The splits are merged by the combine kernel: spread over all SMs it costs less than the
         // in-kernel merge of the pair kernel, which would fall on the last split's CTA pair.
         p.fuse_merge = 0;
@@ -566,7 +575,7 @@ int decode_fwd_impl(const void *q, const void *kv, const float *kv_scale, const 
         e = cudaGetLastError();
         if (e != cudaSuccess) return cuda_fail(e, what);
         if (flags & MLA_FLAG_SKIP_COMBINE) return MLA_OK;
-        return launch_combine(workspace, batch, q_len, num_heads, num_sms, o, lse, 1, p.wait_limit_ns, s);
+        return launch_combine(workspace, batch, q_len, num_heads, num_sms, o, lse, p.sched_id, p.wait_limit_ns, s);
     }
     const int clusters = lay.ctas * lay.groups;
     if (fp8)
@@ -734,7 +743,7 @@ int check_static_ws_args(const void *q, const void *kv, const int32_t *seqlens, 
     }
     if (!aligned(q, 16) || !aligned(kv, 16) || !aligned(o, 16) || !aligned(lse, 4) || !aligned(seqlens, 4))
         return MLA_ERR_ALIGNMENT;
-    if (mla::ws_layout(batch, q_len, num_heads, num_sms).total > (size_t)MLA_STATIC_WORKSPACE_BYTES)
+    if (mla::ws_layout(batch, q_len, num_heads, num_sms).base > (size_t)MLA_STATIC_WORKSPACE_BYTES)
         return MLA_ERR_WORKSPACE;
     return MLA_OK;
 }

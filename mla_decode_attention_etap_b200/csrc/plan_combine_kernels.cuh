@@ -167,8 +167,9 @@ __device__ void plan_schedule_small(int L, int batch, int ctas, int groups, int 
     }
 }
 
-// A CTA of kPlanThreads threads per schedule: CTA 0 the pair schedule, and, for more than 16 query
-// columns, CTA 1 the duo schedule (whose column-group width depends on the shortest nonempty sequence).
+// A CTA of kPlanThreads threads per schedule: CTA 0 the pair schedule, for more than 16 query columns CTA
+// 1 the duo schedule and for more than 64 CTA 2 the tree schedule (whose column-group widths depend on
+// the lengths).
 // The schedules share no table, so the CTAs run side by side (B=16, q_len=4, h=16: 9.5 us one after the
 // other, 6.3 us side by side).  CTA 0 writes the header (and clears the status word) so that the
 // decode kernels can check that they run on a plan for their own grid.
@@ -185,20 +186,28 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int32_t *__res
     const int per = (batch + kPlanThreads - 1) / kPlanThreads;
     const int b0 = min(batch, (int)threadIdx.x * per), b1 = min(batch, b0 + per);
     int mn = 0x7fffffff;  // this thread's shortest nonempty sequence
+    int64_t units = 0;    // and its sequences' units of kDuoRows
     for (int b = b0; b < b1; ++b) {
         const int L = seqlens[b];
         if (L > 0) mn = min(mn, L);
+        units += units_of(L, kDuoRows);
     }
     const int L = per == 1 && b0 < b1 && mn != 0x7fffffff ? mn : 0;  // its only sequence
     int ctas = lay.ctas, groups = lay.groups, mode = 0;
-    if (blockIdx.x == 1) {
+    if (blockIdx.x >= 1) {
         mn = block_min(mn, min_smem);
-        mode = duo_mode(ncols, mn == 0x7fffffff ? 0 : mn);
+        mn = mn == 0x7fffffff ? 0 : mn;
+        mode = duo_mode(ncols, mn);
+        if (blockIdx.x == 2) {
+            int64_t all;
+            block_exclusive_scan(units, sm.scan, &all);
+            mode = tree_mode(ncols, mn, all, num_sms);
+        }
         groups = duo_groups(ncols, mode);
         ctas = num_ctas(num_sms, groups);
     }
-    const Sched &sc = blockIdx.x == 0 ? lay.pair : lay.duo;
-    const int hdr = blockIdx.x == 0 ? kHdrPair : kHdrDuo;
+    const Sched &sc = blockIdx.x == 0 ? lay.pair : blockIdx.x == 1 ? lay.duo : lay.tree;
+    const int hdr = blockIdx.x == 0 ? kHdrPair : blockIdx.x == 1 ? kHdrDuo : kHdrTree;
     const int unit_rows = blockIdx.x == 0 ? kTileRows : kDuoRows;
     const int gcols = blockIdx.x == 0 ? group_cols(ncols) : duo_group_cols(mode);
     if (per == 1 && ctas <= kPlanThreads)
@@ -211,6 +220,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int32_t *__res
         ws[kHdrCols] = ncols;
         ws[kHdrSlotsMax] = lay.slots;
         ws[kHdrSchedUsed] = 0;
+        if (gridDim.x < 3) ws[kHdrTree + kSchCtas] = 0;
     }
 }
 
@@ -218,11 +228,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int32_t *__res
 // thread.  Up to 8 splits' partial LSEs and outputs are loaded at once, so that a sequence with
 // at most 8 splits costs one round trip to L2 once its partials are complete.  Also writes
 // O = 0, LSE = -inf for sequences without rows.
-//   spin = 0: launched after the decode (or by the caller after MLA_FLAG_SKIP_COMBINE): waits
+//   sched = 0: launched after the decode (or by the caller after MLA_FLAG_SKIP_COMBINE): waits
 //             for the whole previous grid (griddepcontrol.wait) and reads the schedule the
 //             decode recorded.
-//   spin = 1: a programmatic dependent of the duo decode kernel that starts on the SMs its CTAs
-//             leave: each CTA waits only for the split counters of its own sequence and column
+//   sched = 1 or 2 (duo or tree): a programmatic dependent of the decode kernel on that schedule
+//             (two CTAs per work unit) that starts on the SMs its CTAs leave: each CTA waits only for the split counters of its own sequence and column
 //             group (both CTAs of every split add 1 with release semantics once their partials
 //             are stored), so early sequences merge while the decode still runs.
 // Either way, for the duo schedule the last combine CTA of a sequence rearms its counters.
@@ -234,20 +244,23 @@ __device__ __forceinline__ int ld_acquire_gpu(const int32_t *p) {
 }
 __global__ void __launch_bounds__(128) combine_kernel(int32_t *__restrict__ ws, const float *__restrict__ opart,
                                                       const float *__restrict__ lsepart, int ncols, WsLayout lay,
-                                                      __nv_bfloat16 *__restrict__ o, float *__restrict__ lse, int spin,
+                                                      __nv_bfloat16 *__restrict__ o, float *__restrict__ lse, int sched,
                                                       unsigned long long wait_limit_ns) {
+    const bool spin = sched != 0;
     if (!spin) asm volatile("griddepcontrol.wait;" ::: "memory");
     const int n = blockIdx.x, b = blockIdx.y;
     // the schedule of the decode that wrote the partials (the plan's tables: complete before the
     // decode started)
-    const bool duo = spin || __ldcg(ws + kHdrSchedUsed) == 1;
-    const Sched &sc = duo ? lay.duo : lay.pair;
+    const int used = spin ? sched : __ldcg(ws + kHdrSchedUsed);
+    const bool duo = used != 0;  // the schedules whose splits are counted for this kernel
+    const Sched &sc = used == 0 ? lay.pair : used == 1 ? lay.duo : lay.tree;
+    const int hdr = used == 2 ? kHdrTree : kHdrDuo;
     const int32_t *seq_info = ws + sc.seq_info / 4;
     const int nsplit = __ldcg(seq_info + 4 * b + 2);
     if (nsplit == 1) return;  // written by the decode kernel
     int32_t *cnt = nullptr;
     if (duo && nsplit >= 2) {
-        const int gcols = __ldcg(ws + kHdrDuo + kSchGroupCols), groups = __ldcg(ws + kHdrDuo + kSchGroups);
+        const int gcols = __ldcg(ws + hdr + kSchGroupCols), groups = __ldcg(ws + hdr + kSchGroups);
         cnt = ws + sc.counters / 4 + ((int64_t)b * groups + n / gcols) * 2;
     }
     if (spin && nsplit >= 2) {
@@ -320,7 +333,7 @@ __global__ void __launch_bounds__(128) combine_kernel(int32_t *__restrict__ ws, 
         lse[(int64_t)b * ncols + n] = lse_tot;
         if (cnt && atomicAdd(ws + sc.done / 4 + b, 1) == ncols - 1) {
             // every combine CTA of this sequence is past its wait: rearm for the next decode
-            const int groups = __ldcg(ws + kHdrDuo + kSchGroups);
+            const int groups = __ldcg(ws + hdr + kSchGroups);
             for (int i = 0; i < 2 * groups; ++i) ws[sc.counters / 4 + (int64_t)b * groups * 2 + i] = 0;
             ws[sc.done / 4 + b] = 0;
         }

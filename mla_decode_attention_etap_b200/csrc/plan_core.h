@@ -8,14 +8,17 @@
 // combines them.  Not on the pages: it exists so that a batch of few long
 // sequences still spreads over every SM.
 //
-// Two schedules live in one workspace:
+// Up to three schedules live in one workspace:
 //   pair  128-row units, column groups of 16 or 32: the CTA-pair kernel (etap_pair_kernel),
 //         used by the FP8 cache for every shape and by the bf16 cache when q_len*h <= 16;
 //   duo   256-row units (a tile of 128 rows per CTA of the pair), column groups of 64 (P as
 //         bf16 hi + lo) or 128 (one bf16 P term): the M = 256 kernel (etap_duo_kernel), used
 //         by the bf16 cache when q_len*h > 16.  Groups of 128 are chosen by the plan, on the
 //         device, when q_len*h > 64 and every nonempty sequence holds at least
-//         kSingleP_MinRows rows; the decode kernel reads the choice from the header.
+//         kSingleP_MinRows rows; the decode kernel reads the choice from the header;
+//   tree  as duo, for tree decodes of more than 64 columns (bf16 and E4M3 cache): groups of 128
+//         also when some sequences are shorter, if there are units enough (tree_mode); the
+//         bf16 kernel then multiplies the short sequences' P as hi and lo, one after the other.
 #pragma once
 
 #include <cstddef>
@@ -45,9 +48,10 @@ enum : int {
     kHdrBatch = 1,
     kHdrCols = 2,
     kHdrSlotsMax = 3,
-    kHdrSchedUsed = 4,   // written by the decode kernel: 0 pair, 1 duo (the partials' schedule)
+    kHdrSchedUsed = 4,   // written by the decode kernel: 0 pair, 1 duo, 2 tree (the partials' schedule)
     kHdrPair = 8,        // + kSch*: the pair schedule
     kHdrDuo = 16,        // + kSch*: the duo schedule
+    kHdrTree = 24,       // + kSch*: the tree schedule (0 units per group: not planned)
     kHdrWords = 64
 };
 enum : int { kSchCtas = 0, kSchGroups = 1, kSchTotal = 2, kSchSlotsUsed = 3, kSchGroupCols = 4, kSchMode = 5 };
@@ -70,6 +74,14 @@ MLA_HD int units_of(int L, int unit_rows) { return L <= 0 ? 0 : (L + unit_rows -
 MLA_HD int tiles_of(int L) { return units_of(L, kTileRows); }
 // The duo mode the plan picks for these lengths (min_len: shortest nonempty sequence, 0 if none).
 MLA_HD int duo_mode(int ncols, int min_len) { return duo_mode1_possible(ncols) && min_len >= kSingleP_MinRows ? 1 : 0; }
+
+// The grouping of the tree schedule: 128 columns wherever the duo schedule takes them, and when every work
+// unit of that grouping gets a unit of KV rows (`units` of kDuoRows in all).  Batches of 16 ragged trees of
+// up to 16 tokens, 16 heads, lengths drawn from 1 to 32768 (three draws each): 194..224 us in groups of
+// 128, 224..269 us in groups of 64.
+MLA_HD int tree_mode(int ncols, int min_len, int64_t units, int num_sms) {
+    return duo_mode(ncols, min_len) || units >= num_ctas(num_sms, duo_groups(ncols, 1)) ? 1 : 0;
+}
 
 // Work units that receive ranges: never more than there are units.
 MLA_HD int used_ctas(int64_t total, int ctas) { return total < (int64_t)ctas ? (int)total : ctas; }
@@ -95,10 +107,11 @@ struct Sched {
 };
 
 struct WsLayout {
-    Sched pair, duo;  // duo is meaningful only when has_duo
-    int has_duo;
+    Sched pair, duo, tree;  // duo is meaningful only when has_duo, tree when has_tree
+    int has_duo, has_tree;
     size_t opart;    // fp32 [slots][ncols][512] (shared: one decode runs per plan at a time)
     size_t lsepart;  // fp32 [2 ranks][slots][ncols] (the two CTAs of a pair compute equal values)
+    size_t base;     // bytes of everything but the tree schedule's tables, which come last
     size_t total;
     int slots;       // batch + the most work units any schedule can have
     // pair schedule grouping (fixed by the shape)
@@ -145,6 +158,9 @@ MLA_HD WsLayout ws_layout(int batch, int q_len, int num_heads, int num_sms) {
     off += align256(sizeof(float) * (size_t)w.slots * ncols * kDv);
     w.lsepart = off;
     off += align256(sizeof(float) * 2 * (size_t)w.slots * ncols);
+    w.base = off;
+    w.has_tree = duo_mode1_possible(ncols) ? 1 : 0;
+    if (w.has_tree) off = sched_tables(w.tree, off, batch, w.duo.ctas_max, w.duo.groups_max, kDuoRows);
     w.total = off;
     return w;
 }

@@ -185,6 +185,38 @@ def test_tree_fp8_needs_scales():
     assert tree(True, scale=0) == -1
 
 
+# ---------------------------------------------------------------------------------- tree schedule
+@pytest.mark.parametrize("lens,q,h,want", [
+    ([1024], 8, 16, (37, 2, 256, 64)),            # 4 units: too few for 74 clusters, groups of 64
+    ([300] * 74, 8, 16, (74, 1, 256, 128)),       # short sequences, but two units for every cluster
+    ([9000], 8, 16, (74, 1, 256, 128)),           # long enough for the duo schedule's groups of 128
+    ([32768] * 16, 4, 16, (74, 1, 256, 64)),      # 64 columns: one group
+    ([64], 64, 16, (4, 16, 256, 64)),             # 1024 columns
+    ([700] * 3, 1, 16, (74, 1, 128, 16)),         # 16 columns: the pair schedule
+])
+def test_tree_schedule_grouping(lens, q, h, want):
+    ranges, info, *rest = m.mla_decode_plan_host(lens, q, h, 148, schedule=2)
+    assert tuple(rest) == want
+    units = sum(-(-L // want[2]) for L in lens)
+    assert ranges[0, 0] == 0 and ranges[-1, 1] == units and (ranges[1:, 0] == ranges[:-1, 1]).all()
+    assert info[:, 0].sum() == units
+
+
+def test_tree_schedule_is_the_duo_schedule_where_its_grouping_is():
+    for lens, q, h in (([9000, 8192], 8, 16), ([100, 20], 8, 16), ([5000] * 3, 4, 16)):
+        a, b = (m.mla_decode_plan_host(lens, q, h, 148, schedule=s) for s in (1, 2))
+        assert a[2:] == b[2:]
+        np.testing.assert_array_equal(a[0], b[0])
+        np.testing.assert_array_equal(a[1], b[1])
+
+
+def test_static_workspace_takes_what_it_took():
+    """The tree schedule's tables come behind what the other decodes need: a workspace without them
+    still serves those, and a tree decode refuses it."""
+    need = m.mla_decode_workspace_size(2, 8, 16, 148)
+    assert tree(q_len=8, ws_bytes=need - 256) == -4 and tree(True, q_len=8, ws_bytes=need - 256) == -4
+
+
 # ------------------------------------------------------------------------------------------ binding
 def i32(*shape):
     return torch.zeros(*shape, dtype=torch.int32)

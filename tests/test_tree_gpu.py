@@ -204,6 +204,51 @@ def test_long_rows_one_probability_term():
     check(w, tree_masks(np.random.default_rng(4), 2, 9), "mode 1")
 
 
+@pytest.mark.parametrize("heads,q_len", [(16, 9), (128, 2), (16, 16)])
+@pytest.mark.parametrize("kv", DTYPES)
+def test_short_sequences_among_enough_units(heads, q_len, kv):
+    """128-column groups with short sequences in them: theirs are multiplied by both bf16 terms of P."""
+    lens = [9000, 700, q_len, 64 + q_len, 3000, 0, 8191, 8192]
+    w = W.make_workload(len(lens), heads, lens, q_len=q_len, paged=True, seed=21, spike_frac=0.03, kv_dtype=kv)
+    q_lens = [q_len if L >= q_len else 0 for L in lens]
+    w.q_lens = torch.tensor(q_lens, dtype=torch.int32)
+    assert m.mla_decode_plan_host(lens, q_len, heads, 148, schedule=2)[5] == 128
+    masks = tree_masks(np.random.default_rng(14), len(lens), q_len)
+    o, lse = check(w, masks, "short among long")
+    # each short sequence by itself, to the same bar
+    o = o.float().cpu().numpy()
+    for b, L in enumerate(lens):
+        if q_lens[b] and L < 8192:
+            r = ref.tree_attention(w.q[b:b + 1].double().numpy(), [rows_of(w, b)], masks[b:b + 1], q_lens[b:b + 1],
+                                   w.softmax_scale)
+            assert_parity(o[b:b + 1], lse[b:b + 1].cpu().numpy(), *r, what=f"L={L}")
+
+
+@pytest.mark.parametrize("batch", [1, 5, 300, 1024, 1025, 3000])
+def test_device_tree_schedule_matches_the_host(batch):
+    from tests.test_parity_gpu import _a256, _sched_offsets
+    rng = np.random.default_rng(batch)
+    for heads, q_len in ((16, 8), (128, 4)):
+        lens = rng.integers(0, 1500, batch).astype(np.int32)
+        dec = m.MlaDecoder(batch, q_len, heads, device="cuda")
+        dec.plan(torch.from_numpy(lens).cuda())
+        torch.cuda.synchronize()
+        ws = dec.workspace.view(torch.int32).cpu().numpy()
+        ncols, sms = heads * q_len, dec.n_sms
+        g64, g128 = (ncols + 63) // 64, (ncols + 127) // 128
+        c_max = max(1, sms // 2 // g128)
+        # the tables are the workspace's last: their size, from the end
+        _, size = _sched_offsets(0, batch, c_max, g64)
+        tab, end = _sched_offsets(dec.workspace.numel() - size, batch, c_max, g64)
+        assert end == dec.workspace.numel()
+        ranges, info, nct, ngr, rows, gcols = m.mla_decode_plan_host(lens, q_len, heads, sms, schedule=2)
+        assert ws[24] == nct and ws[25] == ngr and ws[28] == gcols
+        np.testing.assert_array_equal(ws[tab["ranges"] // 4:][:2 * nct].reshape(-1, 2), ranges)
+        np.testing.assert_array_equal(ws[tab["info"] // 4:][:4 * batch].reshape(-1, 4), info)
+        first = np.concatenate([[0], np.cumsum((lens.astype(np.int64) + rows - 1) // rows)])
+        np.testing.assert_array_equal(ws[tab["tile"] // 4:][:batch + 1], first)
+
+
 def test_bad_pages_are_reported():
     w = W.make_workload(2, 16, [200, 300], q_len=4, paged=True, seed=11)
     w.block_table[1, 2] = 10 ** 6
