@@ -219,8 +219,9 @@ def mla_decode_plan(seqlens: torch.Tensor, q_len: int, num_heads: int, workspace
     _require_cuda(seqlens, "seqlens")
     _require(seqlens, "seqlens", torch.int32, seqlens.device, dim=1)
     _require(workspace, "workspace", None, seqlens.device)
-    _check(lib().mla_decode_plan(_ptr(seqlens), seqlens.numel(), q_len, num_heads, n_sms, _ptr(workspace),
-                                 workspace.numel() * workspace.element_size(), _stream(stream)), "mla_decode_plan")
+    _launch(seqlens.device, stream,
+            lambda s: lib().mla_decode_plan(_ptr(seqlens), seqlens.numel(), q_len, num_heads, n_sms, _ptr(workspace),
+                                            workspace.numel() * workspace.element_size(), s), "mla_decode_plan")
 
 
 def mla_decode_fwd(q, kv, seqlens, block_table, softmax_scale, causal, o, lse, workspace, n_sms, flags=0,
@@ -427,70 +428,99 @@ def mla_combine(workspace, batch, q_len, num_heads, n_sms, o, lse, stream=None) 
     _require(o, "o", torch.bfloat16, o.device, min_numel=batch * q_len * num_heads * D_V)
     _require(lse, "lse", torch.float32, o.device, min_numel=batch * q_len * num_heads)
     _require(workspace, "workspace", None, o.device)
-    _check(lib().mla_combine(_ptr(workspace), batch, q_len, num_heads, n_sms, _ptr(o), _ptr(lse), _stream(stream)),
-           "mla_combine")
+    _launch(o.device, stream,
+            lambda s: lib().mla_combine(_ptr(workspace), batch, q_len, num_heads, n_sms, _ptr(o), _ptr(lse), s),
+            "mla_combine")
 
 
-def _int32(t, name: str, device, shape) -> int:
-    """Address of a contiguous int32 tensor of exactly this shape (None: 0), or TypeError / ValueError."""
+# The checks of the cache operators.  These calls are made for every token, so the accepted case is kept
+# short: `home` is (device, its index as Tensor.get_device() gives it), since comparing indices takes half
+# the time of comparing devices, and the errors are worked out apart.
+def _home(t, name: str):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+    return t.device, t.get_device()
+
+
+def _dense(t, name: str, dtype, home, shape) -> int:
+    """Address of a contiguous tensor of exactly this dtype and shape (None: 0), or TypeError / ValueError."""
     if t is None:
         return 0
     try:
-        if t.dtype is torch.int32 and t.shape == shape and t.device == device and t.is_contiguous():
+        if t.dtype is dtype and t.shape == shape and t.get_device() == home[1] and t.is_contiguous():
             return t.data_ptr()
     except AttributeError:
         pass
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
-    if t.dtype is not torch.int32:
-        raise TypeError(f"{name}: dtype {t.dtype}, expected torch.int32")
-    if t.device != device:
-        raise ValueError(f"{name}: on {t.device}, expected {device} (all tensors on one device)")
-    if t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected contiguous {tuple(shape)}")
-    return t.data_ptr()
+    _require(t, name, dtype, home[0])
+    raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
-def _status_word(status, device) -> int:
+def _int32(t, name: str, home, shape) -> int:
+    return _dense(t, name, torch.int32, home, shape)
+
+
+def _status_word(status, home) -> int:
     try:
-        if status.dtype is torch.int32 and status.device == device and status.is_contiguous() and status.numel():
+        if status.dtype is torch.int32 and status.get_device() == home[1] and status.is_contiguous() and status.numel():
             return status.data_ptr()
     except AttributeError:
         pass
-    _require(status, "status", torch.int32, device, min_numel=1)
+    _require(status, "status", torch.int32, home[0], min_numel=1)
     return status.data_ptr()
 
 
-def _page_stack(block_table, free_pages, num_free, num_free_out, B: int, device):
+def _cache_rows(kv, kv_scale, home) -> tuple:
+    """A cache of 576-wide rows -> (shape, its addresses), codes and scales for the FP8 cache."""
+    fp8 = kv_scale is not None
+    dtype = torch.uint8 if fp8 else torch.bfloat16
+    try:
+        shape = kv.shape
+        good = kv.dtype is dtype and kv.get_device() == home[1] and kv.is_contiguous() and shape[-1] == D_QK
+    except (AttributeError, IndexError):
+        good = False
+    if not good:
+        _require(kv, "kv8" if fp8 else "kv", dtype, home[0], last=D_QK)
+    if not fp8:
+        return shape, [kv.data_ptr()]
+    _require(kv_scale, "kv_scale", torch.float32, home[0], min_numel=math.prod(shape[:-1]))
+    return shape, [kv.data_ptr(), kv_scale.data_ptr()]
+
+
+def _page_stack(block_table, free_pages, num_free, num_free_out, B: int, home):
     """Table and stack of a paged cache -> (table, max_blocks, stack, capacity, count, count out)."""
     if block_table is None:
         return 0, 0, 0, 0, 0, 0
-    _require(block_table, "block_table", torch.int32, device, dim=2)
-    if block_table.shape[0] != B:
-        raise ValueError(f"block_table: {block_table.shape[0]} rows, expected {B}")
-    _require(free_pages, "free_pages", torch.int32, device, dim=1)
-    return (block_table.data_ptr(), block_table.shape[1], free_pages.data_ptr(), free_pages.shape[0],
-            _int32(num_free, "num_free", device, (1,)), _int32(num_free_out, "num_free_out", device, (1,)))
+    if num_free is None or num_free_out is None:
+        raise ValueError("num_free and num_free_out: a paged cache needs both")
+    _home(block_table, "block_table"), _home(free_pages, "free_pages")
+    if block_table.dim() != 2:
+        raise ValueError(f"block_table: {block_table.dim()}-D, expected 2-D")
+    blocks, pages = block_table.shape[1], free_pages.numel()
+    return (_int32(block_table, "block_table", home, (B, blocks)), blocks,
+            _int32(free_pages, "free_pages", home, (pages,)), pages, _int32(num_free, "num_free", home, (1,)),
+            _int32(num_free_out, "num_free_out", home, (1,)))
 
 
 def check_extend_args(seqlens, new_lens, block_table, free_pages, num_free, slots, positions, seqlens_out,
                       num_free_out, status, parents=None, tree_mask=None) -> list:
     """Shapes, dtypes and devices of mla_cache_extend -> the addresses and sizes it passes on."""
-    _require(slots, "slots", torch.int32, slots.device if isinstance(slots, torch.Tensor) else None, dim=2)
-    dev, (B, q_len) = slots.device, slots.shape
+    home = _home(slots, "slots")
+    if slots.dim() != 2:
+        raise ValueError(f"slots: {slots.dim()}-D, expected 2-D")
+    shape = slots.shape
+    B, q_len = shape
     if (parents is None) != (tree_mask is None):
         raise ValueError("parents and tree_mask: give both or neither")
-    if block_table is not None and (num_free is None or num_free_out is None):
-        raise ValueError("num_free and num_free_out: a paged cache needs both")
     if seqlens is None or positions is None or seqlens_out is None:
         raise ValueError("seqlens, positions and seqlens_out are not optional")
+    per_seq = (B,)
     table, max_blocks, stack, capacity, nfree, nfree_out = _page_stack(block_table, free_pages, num_free,
-                                                                       num_free_out, B, dev)
-    return [_int32(seqlens, "seqlens", dev, (B,)), _int32(new_lens, "new_lens", dev, (B,)),
-            _int32(parents, "parents", dev, (B, q_len)), B, q_len, table, max_blocks, stack, capacity, nfree,
-            _int32(positions, "positions", dev, (B, q_len)),
-            _int32(tree_mask, "tree_mask", dev, (B, q_len, _tree_words(q_len))),
-            _int32(seqlens_out, "seqlens_out", dev, (B,)), nfree_out, _status_word(status, dev)]
+                                                                       num_free_out, B, home)
+    return [_int32(seqlens, "seqlens", home, per_seq), _int32(new_lens, "new_lens", home, per_seq),
+            _int32(parents, "parents", home, shape), B, q_len, table, max_blocks, stack, capacity, nfree,
+            _int32(slots, "slots", home, shape), _int32(positions, "positions", home, shape),
+            _int32(tree_mask, "tree_mask", home, (B, q_len, _tree_words(q_len))),
+            _int32(seqlens_out, "seqlens_out", home, per_seq), nfree_out, _status_word(status, home)]
 
 
 def mla_cache_extend(seqlens, new_lens, block_table, free_pages, num_free, kv_rows: int, slots, positions,
@@ -505,54 +535,50 @@ def mla_cache_extend(seqlens, new_lens, block_table, free_pages, num_free, kv_ro
     a = check_extend_args(seqlens, new_lens, block_table, free_pages, num_free, slots, positions, seqlens_out,
                           num_free_out, status, parents, tree_mask)
     _require_cuda(slots, "slots")
-    _launch(slots.device, stream,
-            lambda s: lib().mla_cache_extend(*a[:10], kv_rows, slots.data_ptr(), *a[10:], s), "mla_cache_extend")
+    _launch(slots.device, stream, lambda s: lib().mla_cache_extend(*a[:10], kv_rows, *a[10:], s), "mla_cache_extend")
 
 
 def check_append_args(latent, norm_weight, rope_table, positions, slots, kv, status, q_rope=None, q=None,
                       kv_scale=None) -> tuple:
     """Shapes, dtypes and devices of mla_cache_append(_fp8) -> (arguments ahead of the cache, the cache's,
     those behind it)."""
-    if not isinstance(latent, torch.Tensor):
-        raise TypeError(f"latent: expected a torch.Tensor, got {type(latent).__name__}")
-    dev = latent.device
+    home = _home(latent, "latent")
     if latent.dtype is not torch.bfloat16:
         raise TypeError(f"latent: dtype {latent.dtype}, expected torch.bfloat16")
-    if latent.dim() != 2 or latent.shape[1] != D_QK or (latent.shape[0] > 0 and latent.stride(1) != 1):
-        raise ValueError(f"latent: shape {tuple(latent.shape)}, expected [tokens, {D_QK}] with dense rows")
-    T = latent.shape[0]
-    if norm_weight is not None:
-        _require(norm_weight, "norm_weight", torch.bfloat16, dev, dim=1, last=D_V)
-    _require(rope_table, "rope_table", torch.float32, dev, dim=2, last=64)
+    shape = latent.shape
+    if len(shape) != 2 or shape[1] != D_QK or (shape[0] > 0 and latent.stride(1) != 1):
+        raise ValueError(f"latent: shape {tuple(shape)}, expected [tokens, {D_QK}] with dense rows")
+    T = shape[0]
     if positions is None or slots is None:
         raise ValueError("positions and slots are not optional")
-    fp8 = kv_scale is not None
-    _require(kv, "kv8" if fp8 else "kv", torch.uint8 if fp8 else torch.bfloat16, dev, last=D_QK)
-    rows = kv.numel() // D_QK
-    if fp8:
-        _require(kv_scale, "kv_scale", torch.float32, dev, min_numel=rows)
-    ahead = [latent.data_ptr(), max(latent.stride(0), D_QK) if T <= 1 else latent.stride(0),
-             0 if norm_weight is None else norm_weight.data_ptr()]
-    where = [_int32(positions, "positions", dev, (T,)), _int32(slots, "slots", dev, (T,)), T]
     if (q_rope is None) != (q is None):
         raise ValueError("q_rope and q: give both or neither")
+    max_pos = rope_table.shape[0] if isinstance(rope_table, torch.Tensor) and rope_table.dim() else 0
+    per_token = (T,)
+    weight = _dense(norm_weight, "norm_weight", torch.bfloat16, home, (D_V,))
+    table = _dense(rope_table, "rope_table", torch.float32, home, (max_pos, 64))
+    if not table:
+        raise ValueError("rope_table: not optional, and needs a row")
+    where = [_int32(positions, "positions", home, per_token), _int32(slots, "slots", home, per_token), T]
+    cache_shape, cache = _cache_rows(kv, kv_scale, home)
     queries = [0, 0, 0, 0, 0]
     if q is not None:
-        _require(q, "q", torch.bfloat16, dev, last=D_QK)
-        if not isinstance(q_rope, torch.Tensor):
-            raise TypeError(f"q_rope: expected a torch.Tensor, got {type(q_rope).__name__}")
+        if _home(q_rope, "q_rope") != home:
+            raise ValueError(f"q_rope: on {q_rope.device}, expected {home[0]} (all tensors on one device)")
         if q_rope.dtype is not torch.bfloat16:
             raise TypeError(f"q_rope: dtype {q_rope.dtype}, expected torch.bfloat16")
-        if q_rope.device != dev:
-            raise ValueError(f"q_rope: on {q_rope.device}, expected {dev} (all tensors on one device)")
-        if q_rope.dim() != 3 or q_rope.shape[0] != T or q_rope.shape[2] != 64 or q_rope.stride(2) != 1:
-            raise ValueError(f"q_rope: shape {tuple(q_rope.shape)}, expected [{T}, heads, 64] with dense rows")
-        h = q_rope.shape[1]
-        if q.numel() != T * h * D_QK or q.dim() < 2 or q.shape[-2] != h:
-            raise ValueError(f"q: shape {tuple(q.shape)}, expected [{T}, {h}, {D_QK}] or its tokens as [B, q_len]")
-        queries = [q_rope.data_ptr(), q_rope.stride(0), q_rope.stride(1), h, q.data_ptr()]
-    cache = [kv.data_ptr(), kv_scale.data_ptr(), rows] if fp8 else [kv.data_ptr(), rows]
-    return ahead, [rope_table.data_ptr(), rope_table.shape[0]], where, cache, queries + [_status_word(status, dev)]
+        rs = q_rope.shape
+        if len(rs) != 3 or rs[0] != T or rs[2] != 64 or q_rope.stride(2) != 1:
+            raise ValueError(f"q_rope: shape {tuple(rs)}, expected [{T}, heads, 64] with dense rows")
+        h = rs[1]
+        _home(q, "q")
+        qs = q.shape
+        if math.prod(qs) != T * h * D_QK or len(qs) < 2 or qs[-2] != h or qs[-1] != D_QK:
+            raise ValueError(f"q: shape {tuple(qs)}, expected [{T}, {h}, {D_QK}] or its tokens as [B, q_len]")
+        stride = q_rope.stride()
+        queries = [q_rope.data_ptr(), stride[0], stride[1], h, _dense(q, "q", torch.bfloat16, home, qs)]
+    return ([latent.data_ptr(), latent.stride(0) if T > 1 else D_QK, weight], [table, max_pos], where,
+            cache + [math.prod(cache_shape[:-1])], queries + [_status_word(status, home)])
 
 
 def mla_cache_append(latent, norm_weight, eps, rope_table, interleaved, positions, slots, kv, status, q_rope=None,
@@ -560,9 +586,9 @@ def mla_cache_append(latent, norm_weight, eps, rope_table, interleaved, position
     """Norm the 512 latent columns, rotate the 64 rope columns of each row of ``latent`` ([tokens, 576] bf16,
     rows may be strided) and store the row at ``slots`` of the bf16 cache; with ``q_rope`` ([tokens, heads,
     64], may be strided) also rotate the queries' rope columns into ``q[..., 512:]``."""
-    a = check_append_args(latent, norm_weight, rope_table, positions, slots, kv, status, q_rope, q)
+    ahead, table, where, cache, behind = check_append_args(latent, norm_weight, rope_table, positions, slots, kv,
+                                                           status, q_rope, q)
     _require_cuda(latent, "latent")
-    ahead, table, where, cache, behind = a
     _launch(latent.device, stream,
             lambda s: lib().mla_cache_append(*ahead, eps, *table, int(bool(interleaved)), *where, *cache, *behind, s),
             "mla_cache_append")
@@ -573,9 +599,9 @@ def mla_cache_append_fp8(latent, norm_weight, eps, rope_table, interleaved, posi
     """mla_cache_append into an FP8 cache: E4M3 codes and one fp32 scale per row, max|row| / 448."""
     if kv_scale is None:
         raise TypeError("kv_scale: expected a torch.Tensor, got NoneType")
-    a = check_append_args(latent, norm_weight, rope_table, positions, slots, kv8, status, q_rope, q, kv_scale)
+    ahead, table, where, cache, behind = check_append_args(latent, norm_weight, rope_table, positions, slots, kv8,
+                                                           status, q_rope, q, kv_scale)
     _require_cuda(latent, "latent")
-    ahead, table, where, cache, behind = a
     _launch(latent.device, stream,
             lambda s: lib().mla_cache_append_fp8(*ahead, eps, *table, int(bool(interleaved)), *where, *cache, *behind,
                                                  s),
@@ -585,28 +611,29 @@ def mla_cache_append_fp8(latent, norm_weight, eps, rope_table, interleaved, posi
 def check_accept_args(kv, seqlens, new_lens, path, path_lens, block_table, free_pages, num_free, seqlens_out,
                       num_free_out, status, kv_scale=None) -> tuple:
     """Shapes, dtypes and devices of mla_cache_accept -> (arguments ahead of kv_rows, kv_rows, those behind)."""
-    _require(path, "path", torch.int32, path.device if isinstance(path, torch.Tensor) else None, dim=2)
-    dev, (B, P) = path.device, path.shape
-    fp8 = kv_scale is not None
-    _require(kv, "kv8" if fp8 else "kv", torch.uint8 if fp8 else torch.bfloat16, dev, dim=3, last=D_QK)
-    if fp8:
-        _require(kv_scale, "kv_scale", torch.float32, dev, min_numel=kv.shape[0] * kv.shape[1])
+    home = _home(path, "path")
+    if path.dim() != 2:
+        raise ValueError(f"path: {path.dim()}-D, expected 2-D")
+    B, P = path.shape
+    shape, cache = _cache_rows(kv, kv_scale, home)
+    if len(shape) != 3:
+        raise ValueError(f"kv: {len(shape)}-D, expected 3-D")
     if block_table is not None:
-        if kv.shape[1] != PAGE_SIZE:
-            raise ValueError(f"kv: pages of {kv.shape[1]} rows, expected {PAGE_SIZE}")
-        if num_free is None or num_free_out is None:
-            raise ValueError("num_free and num_free_out: a paged cache needs both")
-    elif kv.shape[0] < B:
-        raise ValueError(f"kv: {kv.shape[0]} sequences, needs at least {B}")
+        if shape[1] != PAGE_SIZE:
+            raise ValueError(f"kv: pages of {shape[1]} rows, expected {PAGE_SIZE}")
+    elif shape[0] < B:
+        raise ValueError(f"kv: {shape[0]} sequences, needs at least {B}")
     if seqlens is None or new_lens is None or path_lens is None or seqlens_out is None:
         raise ValueError("seqlens, new_lens, path_lens and seqlens_out are not optional")
     table, max_blocks, stack, capacity, nfree, nfree_out = _page_stack(block_table, free_pages, num_free,
-                                                                       num_free_out, B, dev)
-    kv_rows = kv.shape[0] * kv.shape[1] if block_table is not None else kv.shape[1]
-    ahead = [kv.data_ptr(), kv_scale.data_ptr() if fp8 else 0, _int32(seqlens, "seqlens", dev, (B,)),
-             _int32(new_lens, "new_lens", dev, (B,)), path.data_ptr(), _int32(path_lens, "path_lens", dev, (B,)), B,
-             2 ** 31 - 1, P, table, max_blocks, stack, capacity, nfree]
-    return ahead, kv_rows, [_int32(seqlens_out, "seqlens_out", dev, (B,)), nfree_out, _status_word(status, dev)]
+                                                                       num_free_out, B, home)
+    per_seq = (B,)
+    ahead = cache + ([] if kv_scale is not None else [0]) + [
+        _int32(seqlens, "seqlens", home, per_seq), _int32(new_lens, "new_lens", home, per_seq),
+        _int32(path, "path", home, (B, P)), _int32(path_lens, "path_lens", home, per_seq), B, 2 ** 31 - 1, P, table,
+        max_blocks, stack, capacity, nfree]
+    return (ahead, shape[0] * shape[1] if block_table is not None else shape[1],
+            [_int32(seqlens_out, "seqlens_out", home, per_seq), nfree_out, _status_word(status, home)])
 
 
 def mla_cache_accept(kv, seqlens, new_lens, path, path_lens, block_table, free_pages, num_free, seqlens_out,
@@ -624,8 +651,8 @@ def mla_cache_accept(kv, seqlens, new_lens, path, path_lens, block_table, free_p
 def mla_decode_read_status(workspace, stream=None) -> int:
     _require_cuda(workspace, "workspace")
     out = ctypes.c_int(0)
-    _check(lib().mla_decode_read_status(_ptr(workspace), ctypes.byref(out), _stream(stream)),
-           "mla_decode_read_status")
+    _launch(workspace.device, stream, lambda s: lib().mla_decode_read_status(_ptr(workspace), ctypes.byref(out), s),
+            "mla_decode_read_status")
     return int(out.value)
 
 
