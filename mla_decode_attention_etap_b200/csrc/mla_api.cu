@@ -359,14 +359,16 @@ int mla_decode_plan(const int32_t *seqlens, int batch, int q_len, int num_heads,
     cudaLaunchConfig_t cfg = {};
     // a CTA per schedule (the tree schedule where the workspace has room for it)
     cfg.gridDim = dim3(1 + lay.has_duo + (lay.has_tree && workspace_bytes >= lay.total ? 1 : 0), 1, 1);
-    cfg.blockDim = dim3(mla::kPlanThreads, 1, 1);
+    const bool warps = batch <= mla::kWarpPlanSeqs && lay.ctas <= mla::kWarpPlanThreads &&
+                       (!lay.has_duo || lay.duo.ctas_max <= mla::kWarpPlanThreads);
+    cfg.blockDim = dim3(warps ? mla::kWarpPlanThreads : mla::kPlanThreads, 1, 1);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, mla::plan_kernel, seqlens, batch, q_len * num_heads, num_sms,
+    cudaError_t e = cudaLaunchKernelEx(&cfg, warps ? mla::plan_warps_kernel : mla::plan_kernel, seqlens, batch, q_len * num_heads, num_sms,
                                        reinterpret_cast<int32_t *>(workspace), lay);
     if (e != cudaSuccess) return cuda_fail(e, "plan_kernel launch");
     e = cudaGetLastError();

@@ -167,12 +167,25 @@ __device__ void plan_schedule_small(int L, int batch, int ctas, int groups, int 
     }
 }
 
-// A CTA of kPlanThreads threads per schedule: CTA 0 the pair schedule, for more than 16 query columns CTA
-// 1 the duo schedule and for more than 64 CTA 2 the tree schedule (whose column-group widths depend on
-// the lengths).
-// The schedules share no table, so the CTAs run side by side (B=16, q_len=4, h=16: 9.5 us one after the
-// other, 6.3 us side by side).  CTA 0 writes the header (and clears the status word) so that the
-// decode kernels can check that they run on a plan for their own grid.
+// The schedules share no table, so a CTA makes each and they run side by side: CTA 0 the pair schedule, for
+// more than 16 query columns CTA 1 the duo schedule and for more than 64 CTA 2 the tree schedule (whose
+// column-group widths depend on the lengths).  CTA 0 writes the header (and clears the status word) so that
+// the decode kernels can check that they run on a plan for their own grid.
+//
+// What bounds a plan is its chain of launch, lengths, sums and table writes.  Three schedules at B = 16,
+// q_len = 4..8, h = 16 (device time of plans in a row): one after the other 9.5 us; a CTA each 6.3; ranges
+// found by a thread each (plan_schedule_small) 4.1..4.4; within warps (plan_warps_kernel) 2.5.
+__device__ __forceinline__ void plan_header(int batch, int ncols, int slots, int32_t *ws) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        ws[kHdrStatus] = 0;
+        ws[kHdrBatch] = batch;
+        ws[kHdrCols] = ncols;
+        ws[kHdrSlotsMax] = slots;
+        ws[kHdrSchedUsed] = 0;
+        if (gridDim.x < 3) ws[kHdrTree + kSchCtas] = 0;
+    }
+}
+
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int32_t *__restrict__ seqlens, int batch, int ncols,
                                                             int num_sms, int32_t *__restrict__ ws, WsLayout lay) {
     // Launched as a programmatic dependent: nothing is read (seqlens may come from the
@@ -214,14 +227,99 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int32_t *__res
         plan_schedule_small(L, batch, ctas, groups, unit_rows, gcols, mode, ws, sc, hdr, sm);
     else
         plan_schedule(seqlens, batch, b0, b1, ctas, groups, unit_rows, gcols, mode, ws, sc, hdr, sm.scan);
-    if (blockIdx.x == 0 && threadIdx.x == 0) {
-        ws[kHdrStatus] = 0;
-        ws[kHdrBatch] = batch;
-        ws[kHdrCols] = ncols;
-        ws[kHdrSlotsMax] = lay.slots;
-        ws[kHdrSchedUsed] = 0;
-        if (gridDim.x < 3) ws[kHdrTree + kSchCtas] = 0;
+    plan_header(batch, ncols, lay.slots, ws);
+}
+
+// The same plan for at most kWarpPlanSeqs sequences and kWarpPlanThreads work units: lane b of every warp owns
+// sequence b, so that sums and searches stay within warps and nothing waits for another warp.  Warp 0
+// writes the sequences' entries, thread c work unit c's range.  2.5 us for three schedules, 2.35 for one,
+// most of it launch; the blocks of plan_kernel take 4.1..4.4 and 2.9 (33 sequences: 3.7).
+constexpr int kWarpPlanThreads = 128, kWarpPlanSeqs = 32;
+__global__ void __launch_bounds__(kWarpPlanThreads) plan_warps_kernel(const int32_t *__restrict__ seqlens, int batch,
+                                                                      int ncols, int num_sms, int32_t *__restrict__ ws,
+                                                                      WsLayout lay) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // as in plan_kernel
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    constexpr uint32_t kAll = 0xffffffffu;
+    const int lane = threadIdx.x & 31, c = threadIdx.x;
+    const int L = lane < batch ? seqlens[lane] : 0;
+    const bool pair = blockIdx.x == 0;
+    const int unit_rows = pair ? kTileRows : kDuoRows;
+    // 32 sequences of fewer than 2^24 units: the sums fit 32 bits
+    const int units = units_of(L, unit_rows), cost = units + (units > 0 ? end_cost_units(unit_rows) : 0);
+    int f = units, g = cost;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int uf = __shfl_up_sync(kAll, f, d), ug = __shfl_up_sync(kAll, g, d);
+        if (lane >= d) f += uf, g += ug;
     }
+    const int total = __shfl_sync(kAll, f, 31), total_cost = __shfl_sync(kAll, g, 31);
+    f -= units;  // first flattened unit, first cost position
+    g -= cost;
+    int ctas = lay.ctas, groups = lay.groups, gcols = group_cols(ncols), mode = 0;
+    if (!pair) {
+        const int shortest = __reduce_min_sync(kAll, L > 0 ? L : 0x7fffffff);
+        const int mn = shortest == 0x7fffffff ? 0 : shortest;
+        mode = blockIdx.x == 1 ? duo_mode(ncols, mn) : tree_mode(ncols, mn, total, num_sms);
+        groups = duo_groups(ncols, mode);
+        ctas = num_ctas(num_sms, groups);
+        gcols = duo_group_cols(mode);
+    }
+    const Sched &sc = pair ? lay.pair : blockIdx.x == 1 ? lay.duo : lay.tree;
+    const int hdr = pair ? kHdrPair : blockIdx.x == 1 ? kHdrDuo : kHdrTree;
+    const int used = used_ctas(total, ctas);
+    // the last of the sequences whose offset (`off` of its lane) is at most x; every lane calls it
+    auto find = [&](int off, int x) -> int {
+        int lo = 0;
+#pragma unroll
+        for (int step = 16; step >= 1; step >>= 1) {
+            const int at = lo + step, v = __shfl_sync(kAll, off, at);
+            if (at < batch && v <= x) lo = at;
+        }
+        return lo;
+    };
+    auto range_start = [&](int r) -> int {
+        const int64_t x = cta_begin(total_cost, used, r);
+        const int q = find(g, (int)x);
+        const int gq = __shfl_sync(kAll, g, q), fq = __shfl_sync(kAll, f, q), uq = __shfl_sync(kAll, units, q);
+        return r < used ? (int)unit_at_cost(x, gq, fq, uq) : total;
+    };
+    const int s = range_start(c), e = range_start(c + 1);
+    const int seq = find(f, s);
+    if (c < ctas) {
+        reinterpret_cast<int2 *>(ws + sc.cta_ranges / 4)[c] = make_int2(s, e);
+        ws[sc.cta_seq / 4 + c] = s < e ? seq : batch;
+    }
+    if (c < 32) {
+        int first = -1, nsplit = 0;
+        if (units > 0) {
+            first = cta_of(total_cost, used, g);
+            nsplit = cta_of(total_cost, used, g + units - 1) - first + 1;
+        }
+        const int mine = nsplit >= 2 ? nsplit : 0;
+        int slot = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int v = __shfl_up_sync(kAll, slot, d);
+            if (lane >= d) slot += v;
+        }
+        if (lane < batch) {
+            ws[sc.tile_off / 4 + lane] = f;
+            reinterpret_cast<int4 *>(ws + sc.seq_info / 4)[lane] = make_int4(units, first, nsplit, slot - mine);
+            ws[sc.done / 4 + lane] = 0;
+        }
+        if (lane == 31) {  // (the inclusive sums of all lanes)
+            ws[sc.tile_off / 4 + batch] = total;
+            ws[hdr + kSchCtas] = ctas;
+            ws[hdr + kSchGroups] = groups;
+            ws[hdr + kSchTotal] = total;
+            ws[hdr + kSchSlotsUsed] = slot;
+            ws[hdr + kSchGroupCols] = gcols;
+            ws[hdr + kSchMode] = mode;
+        }
+    }
+    for (int i = threadIdx.x; i < 2 * batch * groups; i += kWarpPlanThreads) ws[sc.counters / 4 + i] = 0;
+    plan_header(batch, ncols, lay.slots, ws);
 }
 
 // Stand-alone split merge: one CTA of 128 threads per (column, sequence), 4 latent rows per

@@ -224,7 +224,7 @@ def test_short_sequences_among_enough_units(heads, q_len, kv):
             assert_parity(o[b:b + 1], lse[b:b + 1].cpu().numpy(), *r, what=f"L={L}")
 
 
-@pytest.mark.parametrize("batch", [1, 5, 300, 1024, 1025, 3000])
+@pytest.mark.parametrize("batch", [1, 5, 31, 32, 33, 300, 1024, 1025, 3000])
 def test_device_tree_schedule_matches_the_host(batch):
     from tests.test_parity_gpu import _a256, _sched_offsets
     rng = np.random.default_rng(batch)
