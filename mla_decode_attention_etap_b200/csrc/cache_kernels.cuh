@@ -38,6 +38,8 @@ struct ExtendParams {
 // A thread handles TOKENS neighbouring tokens at a time: 4 for many tokens (their lookups in flight
 // together and stored as one; 65536 tokens took 8.2 us with one each and 5.5 us with four), 1 for few
 // (64 tokens of a tree: 3.6 us against 4.9 us, the walks of a thread's tokens running one by one).
+// What bounds it is the chain launch, lengths, sums, barrier, page, stores: 65536 tokens write 0.5 MB, 0.08 us
+// of the measured copy bandwidth.
 template <int TOKENS>
 __global__ void __launch_bounds__(kCacheThreads) extend_kernel(const __grid_constant__ ExtendParams p) {
     __shared__ int64_t scan_smem[32];
@@ -301,7 +303,9 @@ __device__ __forceinline__ void load_angles(const float *table, int pos, int i, 
 // sum of squares is one warp reduction) and two of the rope columns (eight lanes alike), so that the row
 // is read once, kept in registers through norm, rotation and quantisation, and written once.  Queries:
 // four threads per head's 64 columns, each for kQueryHeads heads of one token, with the angles kept in
-// registers across them.
+// registers across them.  Many tokens are bound by HBM: 4096 with 128 heads move 77 MB in 13.3 us, 5.8 TB/s
+// (0.88 of a copy); 8192 E4M3 rows without queries, 16 MB, take 6.7 us (9.1 with the position waited for
+// before the loads, and a division per value), 64 tokens 2.3 us, most of it launch.
 template <bool FP8, bool INTERLEAVED>
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_constant__ AppendParams p) {
     if ((int)blockIdx.x < p.key_blocks) {
@@ -581,7 +585,8 @@ __device__ __forceinline__ void accept_pages(const AcceptParams &p, Wait others_
 
 // A small batch: one cluster.  CTA 0 takes lengths and pages, the warps of the others the rows; they
 // arrive on the cluster barrier as soon as they have read the lengths (all that CTA 0 waits for: the
-// values have been used by then, so the arrival needs no ordering of its own).
+// values have been used by then, so the arrival needs no ordering of its own).  16 sequences of 4 tokens,
+// E4M3: 5.5..6.6 us, the chain lengths, path, page, row, store.
 template <bool FP8>
 __global__ void __launch_bounds__(kCacheThreads) accept_kernel(const __grid_constant__ AcceptParams p) {
     auto arrive = [] { asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory"); };
@@ -604,7 +609,7 @@ __global__ void __launch_bounds__(kCacheThreads) accept_kernel(const __grid_cons
 }
 
 // A large one: a grid of warps, and beside it (a programmatic dependent, which waits for the grid's end
-// before it writes) the CTA for lengths and pages.
+// before it writes) the CTA for lengths and pages.  64 sequences of up to 64 rows: 6.2 us.
 constexpr int kAcceptThreads = 128;
 template <bool FP8>
 __global__ void __launch_bounds__(kAcceptThreads) accept_rows_kernel(const __grid_constant__ AcceptParams p) {

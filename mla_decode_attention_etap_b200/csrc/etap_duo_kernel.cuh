@@ -25,8 +25,18 @@
 //     O^T in TMEM and redo the tile's P^T.
 //   * Column groups of 64 store P as bf16 hi + lo (N = 128 for step 3: [hi | lo] per CTA);
 //     groups of 128 store one bf16 term, used when every sequence of the batch is long enough
-//     (the plan decides; see plan_core.h).
+//     (the plan decides; see plan_core.h).  Tree decodes (TREE) test mask bits in the tiles that
+//     reach into the new rows, and may take groups of 128 with short sequences among them, whose
+//     P is then multiplied as hi and lo in two passes.
 //
+// Measured, kernel and combine: B=32 h=128, 786 MB: 0.219 ms, 3.6 TB/s, 868 TFLOP/s, 0.55 of the HBM
+// roof; B=16 q_len=4 h=16, 604 MB: 0.147 ms, 4.1 TB/s, 0.63; 256 columns on 32768 rows: 1040 TFLOP/s,
+// 0.63 of the tensor roof.  Neither is reached: a unit's chain of loads, scores, votes, P^T and step 3
+// runs over rings of one unit, and shared memory is full.  The tensor pipe is 40..50 % busy.
+//
+// The roles that issue loads and matrix instructions run as whole warps, one elected lane per
+// instruction: a loop run by one lane alone takes 80..130 cycles per instruction, a warp's about 50
+// (B=32 h=128 0.267 -> 0.22 ms with the shorter softmax that it made worth while).
 // Warp roles per CTA (12 warps): 0 loads K tiles and Q (TMA; the bytes of both CTAs count on
 // the even CTA's barriers), 1 issues step 1 (even CTA only) and owns TMEM, 2 loads the value
 // columns for step 3, 3..10 run the softmax and the epilogue (two warps per TMEM lane quadrant,
