@@ -145,6 +145,24 @@ def test_fewer_rows_than_tokens_and_empty_sequences(heads, q_len):
 
 
 @pytest.mark.parametrize("kv", DTYPES)
+@pytest.mark.parametrize("heads,q_len", [(2, 5), (16, 4), (16, 9), (128, 4), (5, 33)])
+def test_padding_queries_and_mask_bits_do_not_matter(heads, q_len, kv):
+    """NaN, infinite and huge queries of padding tokens, and mask bits at or past the count: the same bits."""
+    lens = [700, 9000, q_len, 257]
+    q_lens = [1, q_len - 1, q_len, 0]
+    w = W.make_workload(len(lens), heads, lens, q_len=q_len, paged=True, seed=22, q_lens=q_lens, kv_dtype=kv)
+    masks = random_masks(np.random.default_rng(15), len(lens), q_len)
+    want = run_tree(w, masks)
+    assert want[2] == 0
+    stuff = torch.tensor([float("nan"), float("inf"), -float("inf"), 3e38], dtype=torch.bfloat16)
+    for b, n in enumerate(q_lens):
+        w.q[b, n:] = stuff[torch.arange(w.q[b, n:].numel()) % 4].view(w.q[b, n:].shape)
+        masks[b] = [(row if t < n else 0) | -(1 << n) & (1 << q_len) - 1 for t, row in enumerate(masks[b])]
+    got = run_tree(w, masks)
+    assert got[2] == 0 and torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("kv", DTYPES)
 def test_nan_past_the_end(kv):
     lens = [5, 64, 130, 1000]
     w = W.make_workload(4, 16, lens, q_len=5, paged=True, seed=6, extra_blocks=3, kv_dtype=kv)
