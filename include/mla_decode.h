@@ -398,9 +398,10 @@ MLA_API int mla_decode_read_status(const void *workspace, int *status_out, void 
  * is the one mla_decode_fwd uses: for q_len*h > 16, 256-row units (one 128-row tile per CTA of
  * a pair) and column groups of 64, or of 128 when q_len*h > 64 and every nonempty sequence
  * holds at least 8192 rows (the plan picks this on the device from the same lengths); for
- * q_len*h <= 16 it is schedule 0. `schedule` 2 is the one the tree decodes use: schedule 1, but for
- * q_len*h > 64 with groups of 128 also when the batch has at least one 256-row unit for every work
- * unit of that grouping (mla_decode_fwd_tree_fp8 with q_len*h <= 16 uses schedule 0). Writes, when the pointers are non-NULL:
+ * q_len*h <= 16 it is schedule 0. `schedule` 2 is the one the tree decodes use: for q_len*h <= 16
+ * schedule 0, else as schedule 1 with other costs of a sequence's end, and for q_len*h > 64 with
+ * groups of 128 also when the batch has at least one 256-row unit for every work unit of that
+ * grouping. Writes, when the pointers are non-NULL:
  *   cta_ranges  int32[num_ctas*2]  flattened unit range [begin, end) of each work unit (cut by
  *                                  cost as mla_decode_plan does; possibly empty)
  *   seq_info    int32[batch*4]     per sequence: unit count, first work unit, number of splits, partial slot offset

@@ -281,30 +281,30 @@ int mla_decode_plan_host(const int32_t *seqlens, int batch, int q_len, int num_h
     const mla::WsLayout lay = mla::ws_layout(batch, q_len, num_heads, num_sms);
     const int ncols = q_len * num_heads;
     // schedule 1 (the bf16 cache) is the duo schedule when the shape has one, else the pair schedule;
-    // schedule 2 (tree decodes) the tree schedule when it has one, else that of schedule 1
+    // schedule 2 (tree decodes) likewise the tree schedule
     const bool duo = schedule >= 1 && lay.has_duo;
-    int ctas = lay.ctas, groups = lay.groups, unit_rows = mla::kTileRows, gcols = mla::group_cols(ncols);
+    int ctas = lay.ctas, groups = lay.groups, unit_rows = mla::kTileRows, gcols = mla::group_cols(ncols), mode = 0;
     if (duo) {
         int mn = 0;
         for (int b = 0; b < batch; ++b)
             if (seqlens[b] > 0 && (mn == 0 || seqlens[b] < mn)) mn = seqlens[b];
         int64_t units = 0;
         for (int b = 0; b < batch; ++b) units += mla::units_of(seqlens[b], mla::kDuoRows);
-        const int mode = schedule == 2 && lay.has_tree ? mla::tree_mode(ncols, mn, units, num_sms)
-                                                       : mla::duo_mode(ncols, mn);
+        mode = schedule == 2 ? mla::tree_mode(ncols, mn, units, num_sms) : mla::duo_mode(ncols, mn);
         groups = mla::duo_groups(ncols, mode);
         ctas = mla::num_ctas(num_sms, groups);
         unit_rows = mla::kDuoRows;
         gcols = mla::duo_group_cols(mode);
     }
     // the cost-balanced cut of plan_core.h, sequence by sequence as the plan kernel does it
-    const int E = mla::end_cost_units(unit_rows);
-    int64_t total = 0, total_cost = 0;
+    int64_t total = 0, ends = 0;
     for (int b = 0; b < batch; ++b) {
         const int u = mla::units_of(seqlens[b], unit_rows);
         total += u;
-        total_cost += u + (u > 0 ? E : 0);
+        ends += u > 0;
     }
+    const int E = mla::end_cost_units(duo ? schedule : 0, mode, total, ctas);
+    const int64_t total_cost = total + E * ends;
     if (total > INT32_MAX) return MLA_ERR_UNSUPPORTED;
     const int used = mla::used_ctas(total, ctas);
     std::vector<int32_t> begin((size_t)ctas + 1, (int32_t)total);
@@ -550,7 +550,7 @@ int decode_fwd_impl(const void *q, const void *kv, const float *kv_scale, const 
             if (st != MLA_OK) return st;
         }
         // the plan picks the grouping on the device (see plan_core.h); the kernel reads it from the header
-        const bool tree = tree_mask && lay.has_tree;
+        const bool tree = tree_mask != nullptr;
         const mla::Sched &sc = tree ? lay.tree : lay.duo;
         p.sched_hdr = tree ? mla::kHdrTree : mla::kHdrDuo;
         p.sched_id = tree ? 2 : 1;

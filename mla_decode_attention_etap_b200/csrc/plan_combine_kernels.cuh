@@ -18,24 +18,26 @@ constexpr int kPlanThreads = 1024;
 // per-sequence split info and zeroed merge counters, plus its header words.  Every thread of the
 // block calls it; thread i owns the consecutive sequences [b0, b1).
 __device__ void plan_schedule(const int32_t *__restrict__ seqlens, int batch, int b0, int b1, int ctas, int groups,
-                              int unit_rows, int gcols, int mode, int32_t *__restrict__ ws, const Sched &sc, int hdr,
-                              int64_t *scan_smem) {
+                              int sched, int unit_rows, int gcols, int mode, int32_t *__restrict__ ws,
+                              const Sched &sc, int hdr, int64_t *scan_smem) {
     int32_t *tile_off = ws + sc.tile_off / 4;
     int32_t *ranges = ws + sc.cta_ranges / 4;
     int32_t *seq_info = ws + sc.seq_info / 4;
     int32_t *counters = ws + sc.counters / 4;
     int32_t *cta_seq = ws + sc.cta_seq / 4;
-    const int E = end_cost_units(unit_rows);
     // flattened unit offsets and cost offsets: exclusive prefix sums per sequence
-    int64_t mine = 0, mine_cost = 0;
+    int64_t mine = 0, ends = 0;
     for (int b = b0; b < b1; ++b) {
         const int u = units_of(seqlens[b], unit_rows);
         mine += u;
-        mine_cost += u + (u > 0 ? E : 0);
+        ends += u > 0;
     }
-    int64_t total, total_cost;
+    int64_t total, total_ends;
     int64_t f = block_exclusive_scan(mine, scan_smem, &total);
-    int64_t g = block_exclusive_scan(mine_cost, scan_smem, &total_cost);
+    ends = block_exclusive_scan(ends, scan_smem, &total_ends);
+    const int E = end_cost_units(sched, mode, total, ctas);
+    int64_t g = f + E * ends;
+    const int64_t total_cost = total + E * total_ends;
     const int used = used_ctas(total, ctas);
     for (int c = threadIdx.x; c < ctas; c += blockDim.x) {
         cta_seq[c] = batch;  // no units, unless a sequence below claims it
@@ -102,14 +104,15 @@ struct PlanSmem {
     int64_t f[kPlanThreads], g[kPlanThreads];  // first flattened unit, first cost position
     int32_t start[kPlanThreads + 1];           // first flattened unit of each range
 };
-__device__ void plan_schedule_small(int L, int batch, int ctas, int groups, int unit_rows, int gcols, int mode,
-                                    int32_t *__restrict__ ws, const Sched &sc, int hdr, PlanSmem &sm) {
+__device__ void plan_schedule_small(int L, int batch, int ctas, int groups, int sched, int unit_rows, int gcols,
+                                    int mode, int32_t *__restrict__ ws, const Sched &sc, int hdr, PlanSmem &sm) {
     const int b = threadIdx.x, c = threadIdx.x;
-    const int E = end_cost_units(unit_rows);
     const bool is_seq = b < batch;
     const int64_t units = is_seq ? units_of(L, unit_rows) : 0;
-    int64_t f = units, g = units + (units > 0 ? E : 0), total, total_cost;
-    block_exclusive_scan2(f, g, sm.scan, &total, &total_cost);
+    int64_t f = units, ends = units > 0, total, total_ends;
+    block_exclusive_scan2(f, ends, sm.scan, &total, &total_ends);
+    const int E = end_cost_units(sched, mode, total, ctas);
+    const int64_t g = f + E * ends, total_cost = total + E * total_ends;
     const int used = used_ctas(total, ctas);
     sm.f[b] = f;
     sm.g[b] = g;
@@ -168,8 +171,8 @@ __device__ void plan_schedule_small(int L, int batch, int ctas, int groups, int 
 }
 
 // The schedules share no table, so a CTA makes each and they run side by side: CTA 0 the pair schedule, for
-// more than 16 query columns CTA 1 the duo schedule and for more than 64 CTA 2 the tree schedule (whose
-// column-group widths depend on the lengths).  CTA 0 writes the header (and clears the status word) so that
+// more than 16 query columns CTA 1 the duo schedule and CTA 2 the tree schedule (whose column-group
+// widths depend on the lengths).  CTA 0 writes the header (and clears the status word) so that
 // the decode kernels can check that they run on a plan for their own grid.
 //
 // What bounds a plan is its chain of launch, lengths, sums and table writes.  Three schedules at B = 16,
@@ -224,9 +227,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int32_t *__res
     const int unit_rows = blockIdx.x == 0 ? kTileRows : kDuoRows;
     const int gcols = blockIdx.x == 0 ? group_cols(ncols) : duo_group_cols(mode);
     if (per == 1 && ctas <= kPlanThreads)
-        plan_schedule_small(L, batch, ctas, groups, unit_rows, gcols, mode, ws, sc, hdr, sm);
+        plan_schedule_small(L, batch, ctas, groups, blockIdx.x, unit_rows, gcols, mode, ws, sc, hdr, sm);
     else
-        plan_schedule(seqlens, batch, b0, b1, ctas, groups, unit_rows, gcols, mode, ws, sc, hdr, sm.scan);
+        plan_schedule(seqlens, batch, b0, b1, ctas, groups, blockIdx.x, unit_rows, gcols, mode, ws, sc, hdr, sm.scan);
     plan_header(batch, ncols, lay.slots, ws);
 }
 
@@ -246,16 +249,16 @@ __global__ void __launch_bounds__(kWarpPlanThreads) plan_warps_kernel(const int3
     const bool pair = blockIdx.x == 0;
     const int unit_rows = pair ? kTileRows : kDuoRows;
     // 32 sequences of fewer than 2^24 units: the sums fit 32 bits
-    const int units = units_of(L, unit_rows), cost = units + (units > 0 ? end_cost_units(unit_rows) : 0);
-    int f = units, g = cost;
+    const int units = units_of(L, unit_rows);
+    int f = units;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-        const int uf = __shfl_up_sync(kAll, f, d), ug = __shfl_up_sync(kAll, g, d);
-        if (lane >= d) f += uf, g += ug;
+        const int v = __shfl_up_sync(kAll, f, d);
+        if (lane >= d) f += v;
     }
-    const int total = __shfl_sync(kAll, f, 31), total_cost = __shfl_sync(kAll, g, 31);
-    f -= units;  // first flattened unit, first cost position
-    g -= cost;
+    const int total = __shfl_sync(kAll, f, 31);
+    f -= units;  // first flattened unit
+    const uint32_t nonempty = __ballot_sync(kAll, units > 0);
     int ctas = lay.ctas, groups = lay.groups, gcols = group_cols(ncols), mode = 0;
     if (!pair) {
         const int shortest = __reduce_min_sync(kAll, L > 0 ? L : 0x7fffffff);
@@ -267,7 +270,8 @@ __global__ void __launch_bounds__(kWarpPlanThreads) plan_warps_kernel(const int3
     }
     const Sched &sc = pair ? lay.pair : blockIdx.x == 1 ? lay.duo : lay.tree;
     const int hdr = pair ? kHdrPair : blockIdx.x == 1 ? kHdrDuo : kHdrTree;
-    const int used = used_ctas(total, ctas);
+    const int used = used_ctas(total, ctas), E = end_cost_units(blockIdx.x, mode, total, ctas);
+    const int g = f + E * __popc(nonempty & ((1u << lane) - 1)), total_cost = total + E * __popc(nonempty);
     // the last of the sequences whose offset (`off` of its lane) is at most x; every lane calls it
     auto find = [&](int off, int x) -> int {
         int lo = 0;

@@ -16,9 +16,10 @@
 //         by the bf16 cache when q_len*h > 16.  Groups of 128 are chosen by the plan, on the
 //         device, when q_len*h > 64 and every nonempty sequence holds at least
 //         kSingleP_MinRows rows; the decode kernel reads the choice from the header;
-//   tree  as duo, for tree decodes of more than 64 columns (bf16 and E4M3 cache): groups of 128
-//         also when some sequences are shorter, if there are units enough (tree_mode); the
-//         bf16 kernel then multiplies the short sequences' P as hi and lo, one after the other.
+//   tree  as duo, for tree decodes of more than 16 columns (bf16 and E4M3 cache), with other end
+//         costs (plan_cut.h) and groups of 128 also when some sequences are shorter, if there are
+//         units enough (tree_mode); the bf16 kernel then multiplies the short sequences' P as hi
+//         and lo, one after the other.
 #pragma once
 
 #include <cstddef>
@@ -75,11 +76,12 @@ MLA_HD int tiles_of(int L) { return units_of(L, kTileRows); }
 // The duo mode the plan picks for these lengths (min_len: shortest nonempty sequence, 0 if none).
 MLA_HD int duo_mode(int ncols, int min_len) { return duo_mode1_possible(ncols) && min_len >= kSingleP_MinRows ? 1 : 0; }
 
-// The grouping of the tree schedule: 128 columns wherever the duo schedule takes them, and when every work
+// The grouping of the tree schedule: for more than 64 columns groups of 128 wherever the duo schedule takes them, and when every work
 // unit of that grouping gets a unit of KV rows (`units` of kDuoRows in all).  Batches of 16 ragged trees of
 // up to 16 tokens, 16 heads, lengths drawn from 1 to 32768 (three draws each): 194..224 us in groups of
 // 128, 224..269 us in groups of 64.
 MLA_HD int tree_mode(int ncols, int min_len, int64_t units, int num_sms) {
+    if (!duo_mode1_possible(ncols)) return 0;
     return duo_mode(ncols, min_len) || units >= num_ctas(num_sms, duo_groups(ncols, 1)) ? 1 : 0;
 }
 
@@ -159,7 +161,7 @@ MLA_HD WsLayout ws_layout(int batch, int q_len, int num_heads, int num_sms) {
     w.lsepart = off;
     off += align256(sizeof(float) * 2 * (size_t)w.slots * ncols);
     w.base = off;
-    w.has_tree = duo_mode1_possible(ncols) ? 1 : 0;
+    w.has_tree = w.has_duo;
     if (w.has_tree) off = sched_tables(w.tree, off, batch, w.duo.ctas_max, w.duo.groups_max, kDuoRows);
     w.total = off;
     return w;

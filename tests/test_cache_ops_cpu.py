@@ -202,12 +202,37 @@ def test_tree_schedule_grouping(lens, q, h, want):
     assert info[:, 0].sum() == units
 
 
-def test_tree_schedule_is_the_duo_schedule_where_its_grouping_is():
-    for lens, q, h in (([9000, 8192], 8, 16), ([100, 20], 8, 16), ([5000] * 3, 4, 16)):
+@pytest.mark.parametrize("lens,q,h", [([1024], 8, 16), ([100, 20], 8, 16), ([5000] * 3, 4, 16), ([64], 1, 17),
+                                      ([300, 0, 1], 64, 16)])
+def test_tree_schedule_gives_every_unit_its_own_work_unit(lens, q, h):
+    """As long as there are enough of them."""
+    ranges, info, ctas, *_ = m.mla_decode_plan_host(lens, q, h, 148, schedule=2)
+    units = sum(-(-L // 256) for L in lens)
+    assert units <= ctas
+    assert [tuple(r) for r in ranges] == [(c, c + 1) if c < units else (units, units) for c in range(ctas)]
+    assert info[:, 2].tolist() == [-(-L // 256) for L in lens]
+
+
+def test_tree_schedule_is_the_duo_schedule_in_groups_of_128():
+    for lens, q, h in (([9000, 8192, 10000], 8, 16), ([30000] * 8, 4, 128)):
         a, b = (m.mla_decode_plan_host(lens, q, h, 148, schedule=s) for s in (1, 2))
-        assert a[2:] == b[2:]
+        assert a[5] == 128 and a[2:] == b[2:]
         np.testing.assert_array_equal(a[0], b[0])
         np.testing.assert_array_equal(a[1], b[1])
+
+
+def test_tree_schedule_end_costs():
+    """64-column groups: a sequence's end counts as four units, in the duo schedule as two."""
+    lens = [3000, 5000, 40000, 256, 0, 17]
+    units = [-(-L // 256) for L in lens]
+    for schedule, E in ((1, 2), (2, 4)):
+        ranges, info, ctas, *_ = m.mla_decode_plan_host(lens, 4, 16, 148, schedule=schedule)
+        cost = sum(u + E for u in units if u)
+        # the last unit of every sequence ends a range or lies in one whose cost is at most an even share
+        share = -(-cost // ctas)
+        for lo, hi in ranges:
+            ends = sum(lo < e <= hi for e, u in zip(np.cumsum(units), units) if u)
+            assert hi - lo + E * max(ends - 1, 0) <= share
 
 
 def test_static_workspace_takes_what_it_took():
