@@ -18,7 +18,7 @@
 //     distributed shared memory; in its 128-column groups each takes 64 of the columns and both tiles,
 //     and nothing is merged.
 //
-// B=16, h=16, q_len=4, 16384..32768 rows (230 MB of cache): 84 us with its plan in a row of decodes, 2.7 TB/s (the
+// B=16, h=16, q_len=4, 16384..32768 rows (230 MB of cache): 82 us with its plan in a row of decodes, 2.8 TB/s (the
 // 32-column groups of the pair kernel: 132..179 us on such shapes).  A tile takes a CTA 2.7 us: 1.5 us of matrix
 // instructions, but the chain of its loads (1.2 us after a slot comes free), scores (0.5), softmax (2.0) and
 // step 3 (1.25) runs over a ring of two tiles; shared memory and TMEM are full.
