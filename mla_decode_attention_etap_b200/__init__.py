@@ -217,11 +217,12 @@ def mla_decode_workspace_size(batch: int, q_len: int, num_heads: int, n_sms: int
 def mla_decode_plan(seqlens: torch.Tensor, q_len: int, num_heads: int, workspace: torch.Tensor, n_sms: int,
                     stream=None) -> None:
     _require_cuda(seqlens, "seqlens")
-    _require(seqlens, "seqlens", torch.int32, seqlens.device, dim=1)
-    _require(workspace, "workspace", None, seqlens.device)
-    _launch(seqlens.device, stream,
-            lambda s: lib().mla_decode_plan(_ptr(seqlens), seqlens.numel(), q_len, num_heads, n_sms, _ptr(workspace),
-                                            workspace.numel() * workspace.element_size(), s), "mla_decode_plan")
+    home = seqlens.device
+    _require(seqlens, "seqlens", torch.int32, home, dim=1)
+    _require(workspace, "workspace", None, home)
+    a = (seqlens.data_ptr(), seqlens.numel(), q_len, num_heads, n_sms, workspace.data_ptr(),
+         workspace.numel() * workspace.element_size())
+    _launch(home, stream, lambda s: lib().mla_decode_plan(*a, s), "mla_decode_plan")
 
 
 def mla_decode_fwd(q, kv, seqlens, block_table, softmax_scale, causal, o, lse, workspace, n_sms, flags=0,
@@ -288,15 +289,48 @@ def _tree_words(q_len: int) -> int:
     return (q_len + 31) // 32
 
 
-def check_tree_args(q, kv, seqlens, block_table, tree_mask, o, lse, workspace, q_lens=None, kv_scale=None) -> None:
-    """check_decode_args, and the mask words of every query token."""
-    check_decode_args(q, kv, seqlens, block_table, o, lse, workspace, q_lens, kv_scale)
-    if block_table is not None and kv.shape[1] != PAGE_SIZE:
-        raise ValueError(f"kv: pages of {kv.shape[1]} rows, expected {PAGE_SIZE}")
-    B, q_len = q.shape[:2]
-    _require(tree_mask, "tree_mask", torch.int32, q.device)
-    if tuple(tree_mask.shape) != (B, q_len, _tree_words(q_len)):
-        raise ValueError(f"tree_mask: shape {tuple(tree_mask.shape)}, expected {(B, q_len, _tree_words(q_len))}")
+def check_tree_args(q, kv, seqlens, block_table, tree_mask, o, lse, workspace, q_lens=None, kv_scale=None) -> tuple:
+    """check_decode_args, the page size and the mask words of every query token -> the addresses and sizes
+    that mla_decode_fwd_tree(_fp8) passes on, up to the softmax scale and from the outputs on.
+
+    The conditions are tested in one go (4 us less than one by one); only where one fails does each check run
+    by itself, for its message."""
+    good = False
+    try:
+        index, fp8 = q.get_device(), kv_scale is not None
+        B, q_len, h, width = q.shape
+        rows, per, kv_width = kv.shape
+        columns = B * q_len * h
+        bf16 = torch.bfloat16
+        good = (q.dtype is bf16 and width == D_QK and q.is_contiguous()
+                and kv.dtype is (torch.uint8 if fp8 else bf16) and kv_width == D_QK and kv.get_device() == index
+                and kv.is_contiguous() and _is(seqlens, _INT32, index, B) and seqlens.dim() == 1
+                and (rows >= B if block_table is None else per == PAGE_SIZE and _is(block_table, _INT32, index, 0)
+                     and block_table.dim() == 2 and block_table.shape[0] >= B)
+                and (q_lens is None or _is(q_lens, _INT32, index, B) and q_lens.dim() == 1)
+                and (not fp8 or _is(kv_scale, torch.float32, index, rows * per))
+                and tree_mask.shape == (B, q_len, _tree_words(q_len)) and _is(tree_mask, _INT32, index, 0)
+                and _is(o, bf16, index, columns * D_V) and _is(lse, torch.float32, index, columns)
+                and workspace.get_device() == index and workspace.is_contiguous())
+    except (AttributeError, TypeError, ValueError):
+        pass
+    if not good:
+        check_decode_args(q, kv, seqlens, block_table, o, lse, workspace, q_lens, kv_scale)
+        if block_table is not None and kv.shape[1] != PAGE_SIZE:
+            raise ValueError(f"kv: pages of {kv.shape[1]} rows, expected {PAGE_SIZE}")
+        _require(tree_mask, "tree_mask", torch.int32, q.device)
+        want = (B, q_len, _tree_words(q_len))
+        raise ValueError(f"tree_mask: shape {tuple(tree_mask.shape)}, expected {want}")
+    table, max_blocks = (0, 0) if block_table is None else (block_table.data_ptr(), block_table.shape[1])
+    return [q.data_ptr(), kv.data_ptr()] + ([kv_scale.data_ptr()] if fp8 else []) + [
+        seqlens.data_ptr(), 0 if q_lens is None else q_lens.data_ptr(), tree_mask.data_ptr(), table, B, q_len, h,
+        per if block_table is None else rows * per, max_blocks], [
+        o.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size()]
+
+
+def _is(t, dtype, index: int, min_numel: int) -> bool:
+    """A contiguous tensor of this dtype on this device, with so many elements."""
+    return t.dtype is dtype and t.get_device() == index and t.is_contiguous() and t.numel() >= min_numel
 
 
 def mla_decode_fwd_tree(q, kv, seqlens, block_table, softmax_scale, tree_mask, o, lse, workspace, n_sms, flags=0,
@@ -304,17 +338,9 @@ def mla_decode_fwd_tree(q, kv, seqlens, block_table, softmax_scale, tree_mask, o
     """Decode of drafts that form a tree: token t sees the rows ahead of the q_lens[b] (or q_len) new
     ones and the new tokens u whose bit is set in ``tree_mask`` (int32 [B, q_len, ceil(q_len / 32)])."""
     _require_cuda(q, "q")
-    check_tree_args(q, kv, seqlens, block_table, tree_mask, o, lse, workspace, q_lens)
-    B, q_len, h, _ = q.shape
-    if block_table is not None:
-        kv_rows, max_blocks = kv.shape[0] * kv.shape[1], block_table.shape[1]
-    else:
-        kv_rows, max_blocks = kv.shape[1], 0
-    _launch(q.device, stream,
-            lambda s: lib().mla_decode_fwd_tree(_ptr(q), _ptr(kv), _ptr(seqlens), _ptr(q_lens), _ptr(tree_mask),
-                                                _ptr(block_table), B, q_len, h, kv_rows, max_blocks,
-                                                float(softmax_scale), _ptr(o), _ptr(lse), _ptr(workspace),
-                                                workspace.numel() * workspace.element_size(), n_sms, flags, s),
+    ahead, behind = check_tree_args(q, kv, seqlens, block_table, tree_mask, o, lse, workspace, q_lens)
+    scale = float(softmax_scale)
+    _launch(q.device, stream, lambda s: lib().mla_decode_fwd_tree(*ahead, scale, *behind, n_sms, flags, s),
             "mla_decode_fwd_tree")
 
 
@@ -324,18 +350,9 @@ def mla_decode_fwd_tree_fp8(q, kv8, kv_scale, seqlens, block_table, softmax_scal
     _require_cuda(q, "q")
     if kv_scale is None:
         raise TypeError("kv_scale: expected a torch.Tensor, got NoneType")
-    check_tree_args(q, kv8, seqlens, block_table, tree_mask, o, lse, workspace, q_lens, kv_scale)
-    B, q_len, h, _ = q.shape
-    if block_table is not None:
-        kv_rows, max_blocks = kv8.shape[0] * kv8.shape[1], block_table.shape[1]
-    else:
-        kv_rows, max_blocks = kv8.shape[1], 0
-    _launch(q.device, stream,
-            lambda s: lib().mla_decode_fwd_tree_fp8(_ptr(q), _ptr(kv8), _ptr(kv_scale), _ptr(seqlens), _ptr(q_lens),
-                                                    _ptr(tree_mask), _ptr(block_table), B, q_len, h, kv_rows,
-                                                    max_blocks, float(softmax_scale), _ptr(o), _ptr(lse),
-                                                    _ptr(workspace), workspace.numel() * workspace.element_size(),
-                                                    n_sms, flags, s),
+    ahead, behind = check_tree_args(q, kv8, seqlens, block_table, tree_mask, o, lse, workspace, q_lens, kv_scale)
+    scale = float(softmax_scale)
+    _launch(q.device, stream, lambda s: lib().mla_decode_fwd_tree_fp8(*ahead, scale, *behind, n_sms, flags, s),
             "mla_decode_fwd_tree_fp8")
 
 
