@@ -145,6 +145,17 @@ def test_fewer_rows_than_tokens_and_empty_sequences(heads, q_len):
 
 
 @pytest.mark.parametrize("kv", DTYPES)
+@pytest.mark.parametrize("batch,heads,q_len", [(40, 16, 4), (40, 16, 9), (1100, 10, 3), (1030, 2, 2)])
+def test_large_batches(batch, heads, q_len, kv):
+    """More than 32 sequences, and more than 1024: every way that the plan is made."""
+    lens = np.random.default_rng(batch).integers(0, 400, batch).tolist()
+    lens[3] = 5000
+    q_lens = [min(L, b % (q_len + 1)) for b, L in enumerate(lens)]
+    w = W.make_workload(batch, heads, lens, q_len=q_len, paged=True, seed=24, q_lens=q_lens, kv_dtype=kv)
+    check(w, random_masks(np.random.default_rng(17), batch, q_len), f"batch of {batch}")
+
+
+@pytest.mark.parametrize("kv", DTYPES)
 @pytest.mark.parametrize("heads,q_len", [(2, 5), (16, 4), (16, 9), (128, 4), (5, 33)])
 def test_padding_queries_and_mask_bits_do_not_matter(heads, q_len, kv):
     """NaN, infinite and huge queries of padding tokens, and mask bits at or past the count: the same bits."""
