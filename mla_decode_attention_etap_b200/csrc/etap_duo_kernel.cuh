@@ -572,8 +572,8 @@ __device__ __forceinline__ void duo_body(const DuoMaps &tm, const DecodeParams &
         const float *lx = reinterpret_cast<const float *>(smem + kDuoCtlLx);
         float *mt = reinterpret_cast<float *>(smem + kDuoCtlMt);
         int *vis_s = reinterpret_cast<int *>(smem + kDuoCtlVis);
-        // the peer's vote of unit k lands in slot k & 1 (its vote of unit k + 1 may arrive before this
-        // CTA has read that of unit k)
+        // the peer's vote number v lands in slot v & 1 (its next vote may arrive before this CTA has read
+        // this one)
         const volatile uint32_t *vote_in = reinterpret_cast<const volatile uint32_t *>(smem + kDuoCtlMisc + 64);
         // this thread's P^T row goes to K-half `rank` of the CTA that owns its columns
         const uint32_t p_row_local = C::OFF_P + rank * C::P_BUF + (uint32_t)row * C::P_PITCH;
@@ -586,7 +586,7 @@ __device__ __forceinline__ void duo_body(const DuoMaps &tm, const DecodeParams &
         const uint32_t mx_remote = map_to_rank(sbase + kDuoCtlMx, peer);
         const uint32_t lx_remote = map_to_rank(sbase + kDuoCtlLx, peer);
         bool ok = true, stop = false;
-        int k = 0, kv = 0, xmr = 0, xlr = 0;  // units, passes of step 3, exchange rounds
+        int k = 0, kv = 0, votes = 0, xmr = 0, xlr = 0;  // units, passes of step 3, votes, exchange rounds
         TraceRowT<TR> tr;
         tr.init(p, 3);
         if (tid != 0) tr.row = nullptr;
@@ -730,38 +730,45 @@ __device__ __forceinline__ void duo_body(const DuoMaps &tm, const DecodeParams &
                                tp * kDuoRows + kTileRows * ((int)rank + 1) <= (p.causal ? L - qlen_b + 1 : L) &&
                                grp * NC + NC <= p.ncols;
                     }
-                    // ---- pass 1: does any score exceed its column's running maximum by > 2^THRESH?
-                    float over = -INFINITY;
-                    // rolled: one copy of the score read and test (instruction cache; measured faster)
+                    // ---- pass 1: does any score exceed its column's running maximum by > 2^THRESH?  (A segment's
+                    // first unit sets the maxima: nothing to ask.)
+                    bool slow = first;
+                    if (!first) {
+                        float over = -INFINITY;
+                        // rolled: one copy of the score read and test (instruction cache; measured faster)
 #pragma unroll 1
-                    for (int cc = 0; cc < NH / 32; ++cc) {
-                        float x[32];
-                        load_scores(cc, full, rg, x);
-                        const float4 *nm4 = reinterpret_cast<const float4 *>(nm_s + half * NH + 32 * cc);
+                        for (int cc = 0; cc < NH / 32; ++cc) {
+                            float x[32];
+                            load_scores(cc, full, rg, x);
+                            const float4 *nm4 = reinterpret_cast<const float4 *>(nm_s + half * NH + 32 * cc);
 #pragma unroll
-                        for (int q = 0; q < 8; ++q) {
-                            const float4 nm = nm4[q];
-                            const float2 d0 = add2(make_float2(x[4 * q], x[4 * q + 1]), make_float2(nm.x, nm.y));
-                            const float2 d1 = add2(make_float2(x[4 * q + 2], x[4 * q + 3]), make_float2(nm.z, nm.w));
-                            over = fmaxf(over, fmaxf(fmaxf(d0.x, d0.y), fmaxf(d1.x, d1.y)));
+                            for (int q = 0; q < 8; ++q) {
+                                const float4 nm = nm4[q];
+                                const float2 d0 = add2(make_float2(x[4 * q], x[4 * q + 1]), make_float2(nm.x, nm.y));
+                                const float2 d1 = add2(make_float2(x[4 * q + 2], x[4 * q + 3]), make_float2(nm.z, nm.w));
+                                over = fmaxf(over, fmaxf(fmaxf(d0.x, d0.y), fmaxf(d1.x, d1.y)));
+                            }
                         }
+                        const bool need = !ok || over > kRescaleThreshold;
+                        const bool vote = named_bar_or(SMX, NSM, need);
+                        // ---- votes of both CTAs (a small exchange ahead of P^T, so that P^T is final when written)
+                        if (tid == 0) {
+                            mbar_arrive_expect_tx(bar(BR::XV), 16);
+                            if (ok)
+                                st_async_v4(vote_remote + 16u * (uint32_t)(votes & 1), vote ? 1u : 0u, (uint32_t)k, 0u, 0u,
+                                            xv_remote);
+                        }
+                        ok = ok && spin_phase<true>(bar(BR::XV), votes & 1, wc, status);
+                        slow = vote || vote_in[4 * (votes & 1)] != 0u;
+                        ++votes;
                     }
-                    const bool need = first || !ok || over > kRescaleThreshold;
-                    const bool vote = named_bar_or(SMX, NSM, need);
-                    // ---- votes of both CTAs (a small exchange ahead of P^T, so that P^T is final when written)
-                    if (tid == 0) {
-                        mbar_arrive_expect_tx(bar(BR::XV), 16);
-                        if (ok) st_async_v4(vote_remote + 16u * (uint32_t)(k & 1), vote ? 1u : 0u, (uint32_t)k, 0u, 0u, xv_remote);
-                    }
-                    ok = ok && spin_phase<true>(bar(BR::XV), k & 1, wc, status);
                     tr.put(kEvSmVote, k);
-                    const bool peer_vote = vote_in[4 * (k & 1)] != 0u;
                     // a timed-out wait stops every warp here, before any branch on the peer's vote
                     if (!named_bar_and(SMX, NSM, ok)) {
                         stop = true;
                         break;
                     }
-                    if (named_bar_or(SMX, NSM, vote || peer_vote)) {
+                    if (slow) {  // the same in every thread of both CTAs
                         tr.put(kEvSmSlow, k);
                         // ---- slow path, taken by both CTAs together: tile maxima over all 256 rows
 #pragma unroll 1
@@ -867,12 +874,9 @@ __device__ __forceinline__ void duo_body(const DuoMaps &tm, const DecodeParams &
                 }
                 if (stop) break;
                 // ---------------------------------------------------- epilogue for this CTA's 256 latent rows
-                const int kl = kv - 1;  // the segment's last pass: its step 3 has completed
+                // The column sums are summed and exchanged while the last pass of step 3 runs.
+                const int kl = kv - 1;  // that pass
                 tr.put(kEvSmEpi, kl);
-                ok = ok && spin_phase<false>(bar(BR::PE0), kl & 1, wc, status);
-                ok = ok && spin_phase<false>(bar(BR::PE1), kl & 1, wc, status);
-                tc_fence_after();
-                tr.put(kEvEpiS3, kl);
 #pragma unroll
                 for (int ch = 0; ch < NH / 16; ++ch) {
                     float v16[16];
@@ -890,11 +894,15 @@ __device__ __forceinline__ void duo_body(const DuoMaps &tm, const DecodeParams &
                 }
                 ok = ok && spin_phase<true>(bar(BR::XL), xlr & 1, wc, status);
                 ++xlr;
+                tr.put(kEvEpiL, kl);
+                ok = ok && spin_phase<false>(bar(BR::PE0), kl & 1, wc, status);
+                ok = ok && spin_phase<false>(bar(BR::PE1), kl & 1, wc, status);
                 if (!named_bar_and(SMX, NSM, ok)) {  // also orders the mt writes before the reads
                     stop = true;
                     break;
                 }
-                tr.put(kEvEpiL, kl);
+                tc_fence_after();
+                tr.put(kEvEpiS3, kl);
                 const int nsplit = seg_nsplit;
                 const int slot = seg_slot;
                 // column sum over both CTAs, rank 0's part first in both (identical values)
