@@ -18,7 +18,7 @@
 //     distributed shared memory; in its 128-column groups each takes 64 of the columns and both tiles,
 //     and nothing is merged.
 //
-// B=16, h=16, q_len=4, 16384..32768 rows (230 MB of cache): 82 us with its plan in a row of decodes, 2.8 TB/s (the
+// B=16, h=16, q_len=4, 16384..32768 rows (230 MB of cache): 81 us with its plan in a row of decodes, 2.8 TB/s (the
 // 32-column groups of the pair kernel: 132..179 us on such shapes).  A tile takes a CTA 2.7 us: 1.5 us of matrix
 // instructions, but the chain of its loads (1.2 us after a slot comes free), scores (0.5), softmax (2.0) and
 // step 3 (1.25) runs over a ring of two tiles; shared memory and TMEM are full.
@@ -58,12 +58,14 @@ struct Wide8 {
     static constexpr uint32_t OFF_QV = OFF_ALPHA + 256;  // float[64] 2^-c; the epilogue's of the peer's
     static constexpr uint32_t BYTES = OFF_QV + 256;
     static constexpr uint32_t SMEM_ALLOC = BYTES + 1024;  // slack for 1024-byte alignment
-    // the P^T buffers hold the column maxima or sums of the four lane quadrants while step 3 is idle
+    // the P^T buffers hold the column maxima of the four lane quadrants while step 3 is idle
     static constexpr uint32_t OFF_RED = OFF_P;
     // the Q area receives the peer's part of a segment: 2 M-tiles x 16 column quads x 128 rows x 16 bytes,
     // then its (m, l) per column
     static constexpr uint32_t OFF_XM = OFF_Q, XM_TILE = 128 * NC * 4, OFF_XML = OFF_XM + 2 * XM_TILE;
     static constexpr uint32_t X_BYTES = 2 * XM_TILE + 2 * NC * 4;
+    // and behind that the column sums of the four lane quadrants
+    static constexpr uint32_t OFF_SUM = OFF_XML + 2 * NC * 4;
     static constexpr uint32_t O_COL = 0, S_COL = 4 * NC;  // 4 M-tiles; 2 buffers of [hi | lo] scores
     static constexpr uint32_t IDESC_S = idesc_e4m3_f32(128, 2 * NC, 0, 0);
     static constexpr uint32_t IDESC_O = idesc_e4m3_f32(128, NC, 1, 1);
@@ -73,7 +75,7 @@ struct Wide8 {
                          XFULL = XFREE + 1, BARS = XFULL + 1;
 };
 static_assert(Wide8::SMEM_ALLOC <= 232448 && Wide8::BARS * 8 <= 256 && Wide8::S_COL + 4 * Wide8::NC <= 512 &&
-                  Wide8::OFF_XML + 2 * Wide8::NC * 4 <= Wide8::OFF_P && Wide8::OFF_P % 1024 == 0 &&
+                  Wide8::OFF_SUM + 4 * Wide8::NC * 4 <= Wide8::OFF_P && Wide8::OFF_P % 1024 == 0 &&
                   4 * Wide8::NC * 4 <= 2 * Wide8::P_TERM,
               "shared memory / TMEM plan");
 
@@ -631,22 +633,25 @@ __global__ void __launch_bounds__(Wide8::THREADS, 1)
             }
             if (stop) break;
             // ---------------------------------------------------- epilogue of the segment
+            // Its scores are complete, so the Q area is idle: the peer may send its part there (it hears so
+            // ahead of time), and the column sums are added up behind that, while step 3 of the last tile runs.
+            if (mode == 0 && tid == 0) mbar_arrive_remote(map_to_rank(bar(C::XFREE), peer));
+            float *sums = reinterpret_cast<float *>(smem + C::OFF_SUM);  // [4][64]
+            {
+                const float wsum = warp_colreduce16<false>(lpart, lane);
+                if ((lane & 1) == 0) sums[quad * C::NC + 16 * cq + col16(lane)] = wsum;
+            }
             ok = ok && spin_phase<false>(bar(C::PE), (k - 1) & 1, wc, status);
             if (!named_bar_and(SMX, NSM, ok)) {
                 stop = true;
                 break;
             }
             tc_fence_after();
-            {
-                const float wsum = warp_colreduce16<false>(lpart, lane);
-                if ((lane & 1) == 0) red[quad * C::NC + 16 * cq + col16(lane)] = wsum;
-            }
-            named_bar_sync(SMX, NSM);
             // one thread per column: its sum, (mode 0) both CTAs' parts merged by the log-sum-exp rule, its LSE
             // and the factors of the two parts in the output, P^T's 2^PSCALE included
             float l_own = 0.f;
             if (tid < C::NC)
-                l_own = (red[tid] + red[C::NC + tid]) + (red[2 * C::NC + tid] + red[3 * C::NC + tid]);
+                l_own = (sums[tid] + sums[C::NC + tid]) + (sums[2 * C::NC + tid] + sums[3 * C::NC + tid]);
             auto finish_column = [&](float mm, float l, float as, float ap) {
                 const bool empty = !(l > 0.f);
                 const float inv = empty ? 0.f : C::PUNIT / l;
@@ -695,11 +700,10 @@ __global__ void __launch_bounds__(Wide8::THREADS, 1)
             } else {
                 // The two CTAs hold disjoint rows of the same columns: each finishes latent rows
                 // 256 rank .., so it sends the other two M-tiles and its (m, l) to the peer, into its Q area,
-                // once the peer has said that this area is idle.
+                // once the peer has said that this area is idle (above).
                 const uint32_t x_peer = map_to_rank(sbase + C::OFF_XM, peer);
                 const uint32_t ml_peer = map_to_rank(sbase + C::OFF_XML, peer);
                 const uint32_t xfull_peer = map_to_rank(bar(C::XFULL), peer);
-                if (tid == 0) mbar_arrive_remote(map_to_rank(bar(C::XFREE), peer));
                 ok = ok && spin_phase<true>(bar(C::XFREE), merges & 1, wc, status);
                 if (tid < C::NC && ok) {
                     st_async_b32(ml_peer + 4u * tid, __float_as_uint(m_s[tid]), xfull_peer);
