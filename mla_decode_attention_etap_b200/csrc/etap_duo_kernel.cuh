@@ -29,9 +29,9 @@
 //     reach into the new rows, and may take groups of 128 with short sequences among them, whose
 //     P is then multiplied as hi and lo in two passes.
 //
-// Measured, kernel and combine: B=32 h=128, 786 MB: 0.219 ms, 3.6 TB/s, 868 TFLOP/s, 0.55 of the HBM
-// roof; B=16 q_len=4 h=16, 604 MB: 0.147 ms, 4.1 TB/s, 0.63; 256 columns on 32768 rows: 1040 TFLOP/s,
-// 0.63 of the tensor roof.  Neither is reached: at 64 columns a unit takes 4.1 us, its nine K chunks 3.7
+// Measured, kernel and combine: B=32 h=128, 786 MB: 0.216 ms, 3.6 TB/s, 879 TFLOP/s, 0.56 of the HBM
+// roof; B=16 q_len=4 h=16, 604 MB: 0.144 ms, 4.2 TB/s, 0.64; 256 columns on 32768 rows: 1051 TFLOP/s,
+// 0.64 of the tensor roof.  Neither is reached: at 64 columns a unit takes 4.1 us, its nine K chunks 3.7
 // (1.3 us from a load's issue to its use, four slots) and the chain P^T, step 3, P^T's release 4.0 (step 3
 // waits 0.7 for its third value pair); deeper rings for both do not fit.  16 softmax warps instead of 8
 // took 152 us instead of 150, at 512 columns 196 instead of 185.  The tensor pipe is 40..50 % busy.
