@@ -336,7 +336,10 @@ __global__ void __launch_bounds__(kWarpPlanThreads) plan_warps_kernel(const int3
 //   sched = 1 or 2 (duo or tree): a programmatic dependent of the decode kernel on that schedule
 //             (two CTAs per work unit) that starts on the SMs its CTAs leave: each CTA waits only for the split counters of its own sequence and column
 //             group (both CTAs of every split add 1 with release semantics once their partials
-//             are stored), so early sequences merge while the decode still runs.
+//             are stored), so early sequences merge while the decode still runs.  The grid as a whole does not
+//             complete before the decode does: its last CTA waits for that grid before it exits.  What follows
+//             on the stream (the next plan is a programmatic dependent too) waits for this grid only, and
+//             without that CTA could clear the status word and rewrite the tables under a running decode.
 // Either way, for the duo schedule the last combine CTA of a sequence rearms its counters.
 constexpr int kCombineBatch = 8;
 __device__ __forceinline__ int ld_acquire_gpu(const int32_t *p) {
@@ -344,12 +347,11 @@ __device__ __forceinline__ int ld_acquire_gpu(const int32_t *p) {
     asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
     return v;
 }
-__global__ void __launch_bounds__(128) combine_kernel(int32_t *__restrict__ ws, const float *__restrict__ opart,
-                                                      const float *__restrict__ lsepart, int ncols, WsLayout lay,
-                                                      __nv_bfloat16 *__restrict__ o, float *__restrict__ lse, int sched,
-                                                      unsigned long long wait_limit_ns) {
+__device__ __forceinline__ void combine_column(int32_t *__restrict__ ws, const float *__restrict__ opart,
+                                               const float *__restrict__ lsepart, int ncols, const WsLayout &lay,
+                                               __nv_bfloat16 *__restrict__ o, float *__restrict__ lse, int sched,
+                                               unsigned long long wait_limit_ns) {
     const bool spin = sched != 0;
-    if (!spin) asm volatile("griddepcontrol.wait;" ::: "memory");
     const int n = blockIdx.x, b = blockIdx.y;
     // the schedule of the decode that wrote the partials (the plan's tables: complete before the
     // decode started)
@@ -440,6 +442,16 @@ __global__ void __launch_bounds__(128) combine_kernel(int32_t *__restrict__ ws, 
             ws[sc.done / 4 + b] = 0;
         }
     }
+}
+
+__global__ void __launch_bounds__(128) combine_kernel(int32_t *__restrict__ ws, const float *__restrict__ opart,
+                                                      const float *__restrict__ lsepart, int ncols, WsLayout lay,
+                                                      __nv_bfloat16 *__restrict__ o, float *__restrict__ lse, int sched,
+                                                      unsigned long long wait_limit_ns) {
+    if (sched == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+    combine_column(ws, opart, lsepart, ncols, lay, o, lse, sched, wait_limit_ns);
+    if (sched != 0 && blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1)
+        asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 }  // namespace mla
