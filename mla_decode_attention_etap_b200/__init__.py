@@ -713,9 +713,20 @@ class MlaDecoder:
         self.n_sms = n_sms if n_sms is not None else num_sms(self.device)
         nbytes = mla_decode_workspace_size(batch, q_len, num_heads, self.n_sms)
         self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+        self._planned: Optional[int] = None  # sequences of the last plan
 
     def plan(self, seqlens: torch.Tensor, stream=None):
         mla_decode_plan(seqlens, self.q_len, self.num_heads, self.workspace, self.n_sms, stream)
+        self._planned = seqlens.numel()
+
+    def _tree_shape(self, q) -> tuple:
+        """(batch, q_len, heads) of a tree decode's q, which have to be the planned ones."""
+        B, q_len, h, _ = q.shape
+        if q_len != self.q_len or h != self.num_heads or (self._planned is not None and B != self._planned):
+            batch = self.batch if self._planned is None else self._planned
+            raise ValueError(f"q: {B} sequences of {q_len} tokens and {h} heads, planned for {batch} of {self.q_len} "
+                             f"and {self.num_heads}")
+        return B, q_len, h
 
     def fwd(self, q, kv, seqlens, block_table=None, softmax_scale=None, causal=False, o=None, lse=None,
             flags=0, stream=None, q_lens=None):
@@ -745,7 +756,7 @@ class MlaDecoder:
     def fwd_tree(self, q, kv, seqlens, tree_mask, block_table=None, softmax_scale=None, o=None, lse=None, flags=0,
                  stream=None, q_lens=None):
         """fwd for drafts that form a tree (mask words from mla_cache_extend, or the caller's own)."""
-        B, q_len, h, _ = q.shape
+        B, q_len, h = self._tree_shape(q)
         if o is None:
             o = torch.empty(B, q_len, h, D_V, dtype=torch.bfloat16, device=q.device)
         if lse is None:
@@ -758,7 +769,7 @@ class MlaDecoder:
     def fwd_tree_fp8(self, q, kv8, kv_scale, seqlens, tree_mask, block_table=None, softmax_scale=None, o=None,
                      lse=None, flags=0, stream=None, q_lens=None):
         """fwd_tree over an FP8 cache (E4M3 codes + one fp32 scale per cache row)."""
-        B, q_len, h, _ = q.shape
+        B, q_len, h = self._tree_shape(q)
         if o is None:
             o = torch.empty(B, q_len, h, D_V, dtype=torch.bfloat16, device=q.device)
         if lse is None:

@@ -51,6 +51,7 @@
 #include <type_traits>
 
 #include "etap_common.cuh"
+#include "plan_check.cuh"
 
 namespace mla {
 
@@ -1044,12 +1045,10 @@ __global__ void __launch_bounds__(kDuoThreads, 1)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     // The schedule must come from a plan for this same shape (uniform in the whole cluster).
-    const int mode = p.ws[p.sched_hdr + kSchMode];
-    const int groups = p.ws[p.sched_hdr + kSchGroups];
-    const int ctas = p.ws[p.sched_hdr + kSchCtas];
-    const bool plan_ok = p.ws[kHdrBatch] == p.batch && p.ws[kHdrCols] == p.ncols && (mode == 0 || mode == 1) &&
-                         p.ws[p.sched_hdr + kSchGroupCols] == duo_group_cols(mode) &&
-                         groups == duo_groups(p.ncols, mode) && ctas >= 1 && ctas * groups <= (int)(gridDim.x >> 1);
+    const PlanHeader plan = read_plan_header(p.ws, p.sched_hdr);
+    const int mode = plan.mode, groups = plan.groups, ctas = plan.ctas;
+    const bool plan_ok = duo_plan_matches(plan, p.batch, p.ncols, p.slots, p.ctas) &&
+                         ctas * groups <= (int)(gridDim.x >> 1);
     if (!plan_ok && threadIdx.x == 0) atomicCAS(status, 0, kStatusInvalid);
     if (blockIdx.x == 0 && threadIdx.x == 0) p.ws[kHdrSchedUsed] = p.sched_id;  // the partials' schedule
     const int cluster = (int)(blockIdx.x >> 1);

@@ -7,6 +7,7 @@
 #include "block_scan.cuh"
 #include "etap_common.cuh"
 #include "merge.cuh"
+#include "plan_check.cuh"
 #include "plan_core.h"
 #include "plan_cut.h"
 
@@ -358,15 +359,23 @@ __device__ __forceinline__ void combine_column(int32_t *__restrict__ ws, const f
     const int used = spin ? sched : __ldcg(ws + kHdrSchedUsed);
     const bool duo = used != 0;  // the schedules whose splits are counted for this kernel
     const Sched &sc = used == 0 ? lay.pair : used == 1 ? lay.duo : lay.tree;
-    const int hdr = used == 2 ? kHdrTree : kHdrDuo;
     const int32_t *seq_info = ws + sc.seq_info / 4;
-    const int nsplit = __ldcg(seq_info + 4 * b + 2);
+    // (behind a decode the host has measured the workspace: this word is inside it, whatever it holds)
+    int nsplit = spin ? __ldcg(seq_info + 4 * b + 2) : 0;
+    const PlanHeader plan = read_plan_header(ws, used == 0 ? kHdrPair : used == 2 ? kHdrTree : kHdrDuo);
+    // Tables of another shape, or of no plan at all, are not used: the decode has refused them too.
+    const bool planned = used == 0 ? plan.batch == (int)gridDim.y && plan.ctas == lay.ctas && plan.groups == lay.groups
+                                   : (used == 1 || used == 2) && lay.has_duo &&
+                                         duo_plan_matches(plan, (int)gridDim.y, ncols, lay.slots, sc.ctas_max);
+    if (!planned) {
+        if (threadIdx.x == 0) atomicCAS(ws + kHdrStatus, 0, kStatusInvalid);
+        return;
+    }
+    if (!spin) nsplit = __ldcg(seq_info + 4 * b + 2);
     if (nsplit == 1) return;  // written by the decode kernel
     int32_t *cnt = nullptr;
-    if (duo && nsplit >= 2) {
-        const int gcols = __ldcg(ws + hdr + kSchGroupCols), groups = __ldcg(ws + hdr + kSchGroups);
-        cnt = ws + sc.counters / 4 + ((int64_t)b * groups + n / gcols) * 2;
-    }
+    if (duo && nsplit >= 2)
+        cnt = ws + sc.counters / 4 + ((int64_t)b * plan.groups + n / duo_group_cols(plan.mode)) * 2;
     if (spin && nsplit >= 2) {
         __shared__ int ready;
         if (threadIdx.x == 0) {
@@ -437,7 +446,7 @@ __device__ __forceinline__ void combine_column(int32_t *__restrict__ ws, const f
         lse[(int64_t)b * ncols + n] = lse_tot;
         if (cnt && atomicAdd(ws + sc.done / 4 + b, 1) == ncols - 1) {
             // every combine CTA of this sequence is past its wait: rearm for the next decode
-            const int groups = __ldcg(ws + hdr + kSchGroups);
+            const int groups = plan.groups;
             for (int i = 0; i < 2 * groups; ++i) ws[sc.counters / 4 + (int64_t)b * groups * 2 + i] = 0;
             ws[sc.done / 4 + b] = 0;
         }
