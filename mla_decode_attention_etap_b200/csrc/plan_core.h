@@ -73,7 +73,7 @@ MLA_HD int num_ctas(int num_sms, int groups) {
     int c = num_sms / 2 / groups;
     return c < 1 ? 1 : c;
 }
-MLA_HD int units_of(int L, int unit_rows) { return L <= 0 ? 0 : (L + unit_rows - 1) / unit_rows; }
+MLA_HD int units_of(int L, int unit_rows) { return L <= 0 ? 0 : (L - 1) / unit_rows + 1; }  // (no sum past INT32_MAX)
 MLA_HD int tiles_of(int L) { return units_of(L, kTileRows); }
 // The duo mode the plan picks for these lengths (min_len: shortest nonempty sequence, 0 if none).
 MLA_HD int duo_mode(int ncols, int min_len) { return duo_mode1_possible(ncols) && min_len >= kSingleP_MinRows ? 1 : 0; }
