@@ -249,7 +249,10 @@ __global__ void __launch_bounds__(kWarpPlanThreads) plan_warps_kernel(const int3
     const int L = lane < batch ? seqlens[lane] : 0;
     const bool pair = blockIdx.x == 0;
     const int unit_rows = pair ? kTileRows : kDuoRows;
-    // 32 sequences of fewer than 2^24 units: the sums fit 32 bits
+    // positions on the cost axis fit 32 bits: at most ceil(INT32_MAX / kTileRows) units and 4 end positions a sequence
+    static_assert(kWarpPlanSeqs <= 32 && (int64_t)kWarpPlanSeqs * (0x7fffffff / kTileRows + 1 + 4) <= 0x7fffffff &&
+                      kTileRows <= kDuoRows,
+                  "32-bit sums");
     const int units = units_of(L, unit_rows);
     int f = units;
 #pragma unroll
@@ -284,7 +287,8 @@ __global__ void __launch_bounds__(kWarpPlanThreads) plan_warps_kernel(const int3
         return lo;
     };
     auto range_start = [&](int r) -> int {
-        const int64_t x = cta_begin(total_cost, used, r);
+        // (past the used ranges, and with no rows at all, there is no position to look for)
+        const int64_t x = r < used ? cta_begin(total_cost, used, r) : 0;
         const int q = find(g, (int)x);
         const int gq = __shfl_sync(kAll, g, q), fq = __shfl_sync(kAll, f, q), uq = __shfl_sync(kAll, units, q);
         return r < used ? (int)unit_at_cost(x, gq, fq, uq) : total;

@@ -1,4 +1,4 @@
-"""GPU tests of the plan at the edges of its arithmetic: the longest lengths."""
+"""GPU tests of the plan at the edges of its arithmetic: batches without a row, and the longest lengths."""
 
 from __future__ import annotations
 
@@ -33,6 +33,13 @@ def _tree_tables(lens, heads, q_len):
     return ranges, info
 
 
+@pytest.mark.parametrize("batch", [1, 5, 32, 33])
+@pytest.mark.parametrize("heads,q_len", [(16, 4), (16, 8), (128, 4)])
+def test_plan_of_a_batch_without_rows(batch, heads, q_len):
+    ranges, info = _tree_tables(np.zeros(batch, np.int32), heads, q_len)
+    assert (ranges == 0).all() and (info[:, 0] == 0).all() and (info[:, 2] == 0).all()
+
+
 @pytest.mark.parametrize("batch", [1, 31, 32])
 @pytest.mark.parametrize("heads,q_len", [(16, 4), (128, 4)])
 def test_plan_of_the_longest_lengths(batch, heads, q_len):
@@ -41,3 +48,23 @@ def test_plan_of_the_longest_lengths(batch, heads, q_len):
     lens[2::3] -= 300
     ranges, _ = _tree_tables(lens, heads, q_len)
     assert ranges[-1, 1] == ((lens.astype(np.int64) + 255) // 256).sum()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("heads", [4, 16, 32])
+def test_tree_decode_of_a_batch_without_rows(heads, fp8):
+    B, q_len = 5, 4
+    dec = m.MlaDecoder(B, q_len, heads, device="cuda")
+    lens = torch.zeros(B, dtype=torch.int32, device="cuda")
+    q = torch.randn(B, q_len, heads, 576, device="cuda").bfloat16()
+    kv = torch.zeros(B, 64, 576, dtype=torch.uint8 if fp8 else torch.bfloat16, device="cuda")
+    mask = torch.ones(B, q_len, 1, dtype=torch.int32, device="cuda")
+    o = torch.full((B, q_len, heads, 512), float("nan"), dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((B, q_len, heads), float("nan"), device="cuda")
+    dec.plan(lens)
+    if fp8:
+        dec.fwd_tree_fp8(q, kv, torch.ones(B, 64, device="cuda"), lens, mask, o=o, lse=lse, q_lens=lens)
+    else:
+        dec.fwd_tree(q, kv, lens, mask, o=o, lse=lse, q_lens=lens)
+    assert dec.status() == 0
+    assert (o == 0).all() and torch.isneginf(lse).all()
