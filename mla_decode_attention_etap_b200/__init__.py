@@ -121,6 +121,10 @@ def _check(code: int, what: str):
         raise MlaError(code, what)
 
 
+def _nbytes(t: torch.Tensor) -> int:
+    return t.numel() * t.element_size()
+
+
 def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
@@ -174,12 +178,6 @@ def _require_cuda(t, name: str) -> None:
         raise ValueError(f"{name}: must be a CUDA tensor")
 
 
-def _stream(stream=None):
-    if stream is None:
-        return ctypes.c_void_p(_raw_stream(torch._C._cuda_getDevice()))
-    return ctypes.c_void_p(stream.cuda_stream)
-
-
 def _raw_stream(index: int) -> int:
     """The device's current stream as an address, without building a Stream object (2 us a call)."""
     return torch._C._cuda_getCurrentRawStream(index)
@@ -189,7 +187,7 @@ def _launch(device, stream, call, what: str) -> None:
     """``call(stream pointer)`` with ``device`` current, on ``stream`` or that device's current stream."""
     if stream is None:
         s = _raw_stream(device.index)
-    elif stream.device != device:
+    elif getattr(stream, "device", device) != device:  # (a stream object may name no device)
         raise ValueError(f"{what}: stream on {stream.device}, tensors on {device}")
     else:
         s = stream.cuda_stream
@@ -220,8 +218,7 @@ def mla_decode_plan(seqlens: torch.Tensor, q_len: int, num_heads: int, workspace
     home = seqlens.device
     _require(seqlens, "seqlens", torch.int32, home, dim=1)
     _require(workspace, "workspace", None, home)
-    a = (seqlens.data_ptr(), seqlens.numel(), q_len, num_heads, n_sms, workspace.data_ptr(),
-         workspace.numel() * workspace.element_size())
+    a = (seqlens.data_ptr(), seqlens.numel(), q_len, num_heads, n_sms, workspace.data_ptr(), _nbytes(workspace))
     _launch(home, stream, lambda s: lib().mla_decode_plan(*a, s), "mla_decode_plan")
 
 
@@ -237,16 +234,18 @@ def mla_decode_fwd(q, kv, seqlens, block_table, softmax_scale, causal, o, lse, w
     else:
         kv_rows, max_blocks = kv.shape[1], 0
     if q_lens is None:
-        _check(lib().mla_decode_fwd(_ptr(q), _ptr(kv), _ptr(seqlens), _ptr(block_table), B, q_len, h, kv_rows,
-                                    max_blocks, float(softmax_scale), int(bool(causal)), _ptr(o), _ptr(lse),
-                                    _ptr(workspace), workspace.numel() * workspace.element_size(), n_sms, flags,
-                                    _stream(stream)), "mla_decode_fwd")
+        _launch(q.device, stream,
+                lambda s: lib().mla_decode_fwd(_ptr(q), _ptr(kv), _ptr(seqlens), _ptr(block_table), B, q_len, h,
+                                               kv_rows, max_blocks, float(softmax_scale), int(bool(causal)), _ptr(o),
+                                               _ptr(lse), _ptr(workspace), _nbytes(workspace), n_sms, flags, s),
+                "mla_decode_fwd")
     else:
-        _check(lib().mla_decode_fwd_ragged(_ptr(q), _ptr(kv), _ptr(seqlens), _ptr(q_lens), _ptr(block_table), B,
-                                           q_len, h, kv_rows, max_blocks, float(softmax_scale), int(bool(causal)),
-                                           _ptr(o), _ptr(lse), _ptr(workspace),
-                                           workspace.numel() * workspace.element_size(), n_sms, flags,
-                                           _stream(stream)), "mla_decode_fwd_ragged")
+        _launch(q.device, stream,
+                lambda s: lib().mla_decode_fwd_ragged(_ptr(q), _ptr(kv), _ptr(seqlens), _ptr(q_lens),
+                                                      _ptr(block_table), B, q_len, h, kv_rows, max_blocks,
+                                                      float(softmax_scale), int(bool(causal)), _ptr(o), _ptr(lse),
+                                                      _ptr(workspace), _nbytes(workspace), n_sms, flags, s),
+                "mla_decode_fwd_ragged")
 
 
 def mla_decode_fwd_untransposed(q, kv, seqlens, block_table, softmax_scale, causal, o, lse, workspace, n_sms,
@@ -261,10 +260,12 @@ def mla_decode_fwd_untransposed(q, kv, seqlens, block_table, softmax_scale, caus
         kv_rows, max_blocks = kv.shape[0] * kv.shape[1], block_table.shape[1]
     else:
         kv_rows, max_blocks = kv.shape[1], 0
-    _check(lib().mla_decode_fwd_untransposed(_ptr(q), _ptr(kv), _ptr(seqlens), _ptr(block_table), B, q_len, h,
-                                             kv_rows, max_blocks, float(softmax_scale), int(bool(causal)), _ptr(o),
-                                             _ptr(lse), _ptr(workspace), workspace.numel() * workspace.element_size(),
-                                             n_sms, flags, _stream(stream)), "mla_decode_fwd_untransposed")
+    _launch(q.device, stream,
+            lambda s: lib().mla_decode_fwd_untransposed(_ptr(q), _ptr(kv), _ptr(seqlens), _ptr(block_table), B, q_len,
+                                                        h, kv_rows, max_blocks, float(softmax_scale),
+                                                        int(bool(causal)), _ptr(o), _ptr(lse), _ptr(workspace),
+                                                        _nbytes(workspace), n_sms, flags, s),
+            "mla_decode_fwd_untransposed")
 
 
 def mla_decode_fwd_fp8(q, kv8, kv_scale, seqlens, block_table, softmax_scale, causal, o, lse, workspace, n_sms,
@@ -278,11 +279,12 @@ def mla_decode_fwd_fp8(q, kv8, kv_scale, seqlens, block_table, softmax_scale, ca
         kv_rows, max_blocks = kv8.shape[0] * kv8.shape[1], block_table.shape[1]
     else:
         kv_rows, max_blocks = kv8.shape[1], 0
-    _check(lib().mla_decode_fwd_fp8(_ptr(q), _ptr(kv8), _ptr(kv_scale), _ptr(seqlens), _ptr(q_lens),
-                                    _ptr(block_table), B, q_len, h, kv_rows, max_blocks, float(softmax_scale),
-                                    int(bool(causal)), _ptr(o), _ptr(lse), _ptr(workspace),
-                                    workspace.numel() * workspace.element_size(), n_sms, flags, _stream(stream)),
-           "mla_decode_fwd_fp8")
+    _launch(q.device, stream,
+            lambda s: lib().mla_decode_fwd_fp8(_ptr(q), _ptr(kv8), _ptr(kv_scale), _ptr(seqlens), _ptr(q_lens),
+                                               _ptr(block_table), B, q_len, h, kv_rows, max_blocks,
+                                               float(softmax_scale), int(bool(causal)), _ptr(o), _ptr(lse),
+                                               _ptr(workspace), _nbytes(workspace), n_sms, flags, s),
+            "mla_decode_fwd_fp8")
 
 
 def _tree_words(q_len: int) -> int:
@@ -375,10 +377,11 @@ def mla_decode_fwd_trace(q, kv, seqlens, block_table, softmax_scale, causal, o, 
         kv_rows, max_blocks = kv.shape[0] * kv.shape[1], block_table.shape[1]
     else:
         kv_rows, max_blocks = kv.shape[1], 0
-    _check(lib().mla_decode_fwd_trace(_ptr(q), _ptr(kv), _ptr(seqlens), _ptr(block_table), B, q_len, h, kv_rows,
-                                      max_blocks, float(softmax_scale), int(bool(causal)), _ptr(o), _ptr(lse),
-                                      _ptr(workspace), workspace.numel() * workspace.element_size(), n_sms,
-                                      _ptr(trace), cap, _stream(stream)), "mla_decode_fwd_trace")
+    _launch(q.device, stream,
+            lambda s: lib().mla_decode_fwd_trace(_ptr(q), _ptr(kv), _ptr(seqlens), _ptr(block_table), B, q_len, h,
+                                                 kv_rows, max_blocks, float(softmax_scale), int(bool(causal)), _ptr(o),
+                                                 _ptr(lse), _ptr(workspace), _nbytes(workspace), n_sms, _ptr(trace),
+                                                 cap, s), "mla_decode_fwd_trace")
 
 
 def trace_buffer(cap: int, n_sms: int, device=None):
@@ -427,7 +430,8 @@ def mla_stream_probe(kv, units: int, err, stream=None) -> None:
     _require(kv, "kv", torch.bfloat16, kv.device, last=D_QK)
     _require(err, "err", torch.int32, kv.device, min_numel=1)
     rows = kv.numel() // 576
-    _check(lib().mla_stream_probe(_ptr(kv), rows, units, _ptr(err), _stream(stream)), "mla_stream_probe")
+    _launch(kv.device, stream,
+            lambda s: lib().mla_stream_probe(_ptr(kv), rows, units, _ptr(err), s), "mla_stream_probe")
 
 
 def mla_form_ablation(form: int, heads: int, streams: int, tiles: int, cycles, err, stream=None) -> None:
@@ -436,8 +440,9 @@ def mla_form_ablation(form: int, heads: int, streams: int, tiles: int, cycles, e
     _require_cuda(cycles, "cycles")
     _require(cycles, "cycles", torch.int64, cycles.device, min_numel=1)
     _require(err, "err", torch.int32, cycles.device, min_numel=1)
-    _check(lib().mla_form_ablation(form, heads, streams, tiles, cycles.numel(), _ptr(cycles), _ptr(err),
-                                   _stream(stream)), "mla_form_ablation")
+    _launch(cycles.device, stream,
+            lambda s: lib().mla_form_ablation(form, heads, streams, tiles, cycles.numel(), _ptr(cycles), _ptr(err), s),
+            "mla_form_ablation")
 
 
 def mla_combine(workspace, batch, q_len, num_heads, n_sms, o, lse, stream=None) -> None:
