@@ -127,8 +127,9 @@ struct PairCfg {
     static constexpr uint32_t TMEM_COLS = pow2_at_least(MB * NP + 2 * NS);
     static constexpr uint32_t IDESC_QK = KV8 ? idesc_e4m3_f32(128, NS, 0, 0) : idesc_bf16_f32(128, NG, 0, 0);
     static constexpr uint32_t IDESC_PV = KV8 ? idesc_e4m3_f32(128, NP, 1, 1) : idesc_bf16_f32(128, NP, 1, 1);
-    static constexpr float THRESH = KV8 ? kRescaleThreshold8 : kRescaleThreshold;
-    static constexpr float HEADROOM = KV8 ? kRescaleHeadroom8 : kRescaleHeadroom;
+    // a row that passes m by this moves it; bf16: to this above the tile's largest
+    static constexpr float THRESH = KV8 ? kTopLog2_8 - kPScaleLog2_8 : kRescaleThreshold;
+    static constexpr float HEADROOM = kRescaleHeadroom;
     // The in-kernel split merge stages (splits + 1) x NG floats in the idle P^T buffers.
     static constexpr int MERGE_MAX_SPLITS = (int)(STAGE_BYTES / 4) / NG - 1;
 };
@@ -796,7 +797,13 @@ __global__ void __launch_bounds__(320, 1)
 #pragma unroll
                     for (int n = 0; n < NH; ++n) qv[n] = 1.f;
                 }
-                for (int t = t0 + toff; t < t1 && !stop; t += C::TSTEP, ++k) {
+                // E4M3: the tiles of the segment in which this thread's columns look, and the largest x of each so far as
+                // looked at (see etap_common.cuh)
+                int seen_tiles = 0, look_at = 0, look_gap = 1;
+                float highest[C::KV8 ? NH : 1];
+#pragma unroll
+                for (int n = 0; n < (C::KV8 ? NH : 1); ++n) highest[n] = -INFINITY;
+                for (int t = t0 + toff; t < t1 && !stop; t += C::TSTEP, ++k, ++seen_tiles) {
                     const bool first = (t == t0 + toff);
                     const int pb = k % C::PB;
                     ok = ok && spin_phase<false>(bar(BR::SFULL + (k & 1)), (k >> 1) & 1, wc, status);
@@ -805,7 +812,7 @@ __global__ void __launch_bounds__(320, 1)
                     const int rg = t * kTileRows + row;
                     // E4M3: this row's scale s (from the rope slot, which the warps then free); the row's scores
                     // are s * (K codes . Q terms) * 2^-c_n, and the maximum tracks them plus log2 s
-                    float rsq[NH], lgs = 0.f, inv16 = 1.f;
+                    float rsq[NH], lgs = 0.f, unstore = 1.f;
                     if constexpr (C::KV8) {
                         const int rsl = k % C::NR;
                         ok = ok && spin_phase<false>(bar(BR::RFULL + rsl), (k / C::NR) & 1, wc, status);
@@ -815,7 +822,7 @@ __global__ void __launch_bounds__(320, 1)
                         if (lane == 0) mbar_arrive(bar(BR::REMPTY + rsl));
                         sig = rg < L ? fmaxf(sig, 0x1p-100f) : 1.f;
                         lgs = __log2f(sig);
-                        inv16 = 0.0625f / sig;  // 2^-4 / s: turns a stored p back into 2^(score - m)
+                        unstore = kPUnit8 / sig;  // 2^-PSCALE / s: turns a stored p back into 2^(score - m)
                         const float rsc = sig * p.scale_log2;
 #pragma unroll
                         for (int n = 0; n < NH; ++n) rsq[n] = rsc * qv[n];
@@ -905,7 +912,7 @@ __global__ void __launch_bounds__(320, 1)
                         }
                     }
                     // ---- pass 1: full scores of this thread's columns (exchange for CH == 1), scale + mask
-                    bool need = first || !ok;
+                    bool need = (C::KV8 ? seen_tiles == look_at : first) || !ok;
 #pragma unroll
                     for (int ch = 0; ch < C::CH; ++ch) {
                         float(&x)[8] = xc[ch];
@@ -965,7 +972,8 @@ __global__ void __launch_bounds__(320, 1)
                     }
                     // ---- one vote per tile; the slow path takes the column maxima of all chunks
                     float alpha[C::CH][8];
-                    bool rescale = false;
+                    bool rescale = false, jumped = false;
+                    const bool look = seen_tiles == look_at;  // (E4M3)
 #pragma unroll
                     for (int ch = 0; ch < C::CH; ++ch)
 #pragma unroll
@@ -999,7 +1007,23 @@ __global__ void __launch_bounds__(320, 1)
 #pragma unroll
                                 for (int u = 0; u < 4; ++u) {
                                     const int n = n4 + u, li = 8 * ch + n;
-                                    if (first) {
+                                    if constexpr (C::KV8) {
+                                        const float h0 = fmaxf(u == 0 ? a.x : u == 1 ? a.y : u == 2 ? a.z : a.w,
+                                                               u == 0 ? bq.x : u == 1 ? bq.y : u == 2 ? bq.z : bq.w);
+                                        const float h1 = fmaxf(u == 0 ? c.x : u == 1 ? c.y : u == 2 ? c.z : c.w,
+                                                               u == 0 ? d.x : u == 1 ? d.y : u == 2 ? d.z : d.w);
+                                        highest[li] = fmaxf(highest[li], mt4[u]);
+                                        const float from = m[li] == -INFINITY ? kNoRow : kPScaleLog2_8 - m[li];
+                                        const float to = follow_maximum8(from, h0, h1, highest[li], look);
+                                        if (to != from) {
+                                            m[li] = kPScaleLog2_8 - to;
+                                            if (!first) {  // (a first tile's O^T does not exist yet)
+                                                alpha[ch][n] = fast_exp2(to - from);  // 0: a column without a row so far
+                                                rescale = true;
+                                                jumped = jumped || mt4[u] + from > kTopLog2_8 + kJump8;
+                                            }
+                                        }
+                                    } else if (first) {
                                         m[li] = mt4[u] + C::HEADROOM;
                                     } else if (mt4[u] > m[li] + C::THRESH) {
                                         alpha[ch][n] = fast_exp2(m[li] - (mt4[u] + C::HEADROOM));
@@ -1008,6 +1032,13 @@ __global__ void __launch_bounds__(320, 1)
                                     }
                                 }
                             }
+                        }
+                        if (jumped) {
+                            look_at = seen_tiles + 1;
+                            look_gap = kLookStep8;
+                        } else if (look) {
+                            look_at = seen_tiles + look_gap;
+                            look_gap *= kLookStep8;
                         }
                     }
                     // ---- pass 2: probabilities, P^T (hi + lo) into shared memory, O^T rescale
@@ -1019,9 +1050,9 @@ __global__ void __launch_bounds__(320, 1)
                             const int li = 8 * ch + n;
                             const float mu = (m[li] == -INFINITY) ? 0.f : m[li];
                             if constexpr (C::KV8) {
-                                // stored p = 2^(score + log2 s - m + 4); the sum takes 2^(score - m)
+                                // stored p = 2^(score + log2 s - m + PSCALE); the sum takes 2^(score - m)
                                 pv[n] = fast_exp2(xc[ch][n] - (mu - kPScaleLog2_8));
-                                lpart[li] = fmaf(pv[n], inv16, lpart[li] * alpha[ch][n]);
+                                lpart[li] = fmaf(pv[n], unstore, lpart[li] * alpha[ch][n]);
                             } else {
                                 pv[n] = fast_exp2(xc[ch][n] - mu);
                                 lpart[li] = lpart[li] * alpha[ch][n] + pv[n];
@@ -1037,7 +1068,9 @@ __global__ void __launch_bounds__(320, 1)
                             for (int i = 0; i < 4; ++i) {
                                 const uint16_t h = f32x2_to_e4m3x2(pv[2 * i], pv[2 * i + 1]);
                                 const float2 hf = e4m3x2_to_f32x2(h);
-                                const uint16_t l = f32x2_to_e4m3x2(pv[2 * i] - hf.x, pv[2 * i + 1] - hf.y);
+                                const float2 rest = add2(make_float2(pv[2 * i], pv[2 * i + 1]),
+                                                         make_float2(dither8(row), dither8(row)));
+                                const uint16_t l = f32x2_to_e4m3x2(rest.x - hf.x, rest.y - hf.y);
                                 hi[i >> 1] |= (uint32_t)h << (16 * (i & 1));
                                 lo[i >> 1] |= (uint32_t)l << (16 * (i & 1));
                             }
@@ -1251,8 +1284,8 @@ __global__ void __launch_bounds__(320, 1)
                             const float l = rank == 0 ? __fmaf_rn(ls[li], as, __fmul_rn(lp, ap))
                                                       : __fmaf_rn(lp, ap, __fmul_rn(ls[li], as));
                             const bool empty = !(l > 0.f) || mm == -INFINITY;
-                            // the stored p carried a factor 2^4
-                            const float inv = empty ? 0.f : 0.0625f / l;
+                            // the stored p carried a factor 2^PSCALE
+                            const float inv = empty ? 0.f : kPUnit8 / l;
                             lse_n[n] = empty ? -INFINITY : (mm + __log2f(l)) * 0.69314718055994531f;
 #pragma unroll
                             for (int j = 0; j < 2; ++j) {

@@ -37,13 +37,6 @@ struct Wide8 {
     static constexpr int NC = 64;                      // query columns of a CTA
     static constexpr int NV = 8;                       // 16 KB slots: 128 rows x 128 codes
     static constexpr int THREADS = 640, NSM = 512;     // softmax threads: warps 4..19
-    // P^T is stored times 2^PSCALE.  m is set HEADROOM above a tile's maximum and moves once a row exceeds it
-    // by THRESH, so that a stored p is at most 2^(THRESH + PSCALE) = 256 (E4M3 ends at 448) and the largest of
-    // a column, right after m moved, is 2^(PSCALE - HEADROOM) = 16.  The low term resolves 2^-10, 2^-14 of
-    // that: the rows around a sequence's typical score, some 2^-5 of its largest, keep the 8 bits of two
-    // E4M3 terms.  (With 4, 2 and 4 in their places, 2^-12: the error of O over 3000 rows was 2.0e-3 of its
-    // RMS, bf16's rounding of O alone being 1.65e-3.)
-    static constexpr float PSCALE = 5.f, PUNIT = 0.03125f, THRESH = 3.f, HEADROOM = 1.f;
     static constexpr uint32_t CHUNK = 16384, HALF = 8192;
     static constexpr uint32_t R_ROW = 64, R_DATA = 128 * R_ROW, R_HALF = 64 * R_ROW;
     static constexpr uint32_t Q_CHUNK = 2 * NC * 128, P_TERM = 128 * NC;
@@ -54,13 +47,12 @@ struct Wide8 {
     static constexpr uint32_t OFF_P = OFF_QR + 2 * NC * R_ROW;  // P_hi, then P_lo
     static constexpr uint32_t OFF_BAR = OFF_P + 2 * P_TERM;
     static constexpr uint32_t OFF_MISC = OFF_BAR + 256;  // +0 TMEM address, +16 WaitCtl
-    static constexpr uint32_t OFF_M = OFF_MISC + 64;     // float[64] PSCALE minus the running maximum m (log2 units)
+    static constexpr uint32_t OFF_M = OFF_MISC + 64;     // float[64] PSCALE - m (log2 units)
     static constexpr uint32_t OFF_ALPHA = OFF_M + 256;   // float[64] rescale factors; the epilogue's factors of this CTA's part
     static constexpr uint32_t OFF_QV = OFF_ALPHA + 256;  // float[64] 2^-c; the epilogue's of the peer's
-    static constexpr uint32_t BYTES = OFF_QV + 256;
+    static constexpr uint32_t OFF_MX = OFF_QV + 256;     // int[2][64] column maxima of a tile's halves (ordered_bits)
+    static constexpr uint32_t BYTES = OFF_MX + 512;
     static constexpr uint32_t SMEM_ALLOC = BYTES + 1024;  // slack for 1024-byte alignment
-    // the P^T buffers hold the column maxima of the four lane quadrants while step 3 is idle
-    static constexpr uint32_t OFF_RED = OFF_P;
     // the Q area receives the peer's part of a segment: 2 M-tiles x 16 column quads x 128 rows x 16 bytes,
     // then its (m, l) per column
     static constexpr uint32_t OFF_XM = OFF_Q, XM_TILE = 128 * NC * 4, OFF_XML = OFF_XM + 2 * XM_TILE;
@@ -76,9 +68,12 @@ struct Wide8 {
                          XFULL = XFREE + 1, BARS = XFULL + 1;
 };
 static_assert(Wide8::SMEM_ALLOC <= 232448 && Wide8::BARS * 8 <= 256 && Wide8::S_COL + 4 * Wide8::NC <= 512 &&
-                  Wide8::OFF_SUM + 4 * Wide8::NC * 4 <= Wide8::OFF_P && Wide8::OFF_P % 1024 == 0 &&
-                  4 * Wide8::NC * 4 <= 2 * Wide8::P_TERM,
+                  Wide8::OFF_SUM + 4 * Wide8::NC * 4 <= Wide8::OFF_P && Wide8::OFF_P % 1024 == 0,
               "shared memory / TMEM plan");
+
+// An int that orders as the float does (its own inverse), for a maximum over warps by atomicMax.
+__device__ __forceinline__ int ordered_bits(int bits) { return bits < 0 ? bits ^ 0x7fffffff : bits; }
+constexpr int kOrderedLowest = (int)0x80000000;  // below every float's
 
 // The 128-row tiles of a CTA, segment by segment: tile t of the segments' sequence b.
 struct WideTiles {
@@ -399,7 +394,8 @@ __global__ void __launch_bounds__(Wide8::THREADS, 1)
         float *m_s = reinterpret_cast<float *>(smem + C::OFF_M);
         float *alpha_s = reinterpret_cast<float *>(smem + C::OFF_ALPHA);
         float *qv_s = reinterpret_cast<float *>(smem + C::OFF_QV);
-        float *red = reinterpret_cast<float *>(smem + C::OFF_RED);  // [4][64]
+        int *mx_s = reinterpret_cast<int *>(smem + C::OFF_MX);
+        if (tid < 2 * C::NC) mx_s[tid] = kOrderedLowest;
         bool ok = true, stop = false;
         int k = 0, seg = 0, merges = 0;
         WideTiles w;
@@ -509,7 +505,10 @@ __global__ void __launch_bounds__(Wide8::THREADS, 1)
                 rq[n] = qv_s[16 * cq + n] * p.scale_log2;
             }
             bool more = true;
-            for (; more; ++k) {
+            // the tiles of the segment in which a column (that of this thread, if it has one) looks, see etap_common.cuh
+            int seen_tiles = 0, look_at = tid < C::NC ? 0 : -1, look_gap = 1;
+            float highest = -INFINITY;
+            for (; more; ++k, ++seen_tiles) {
                 const bool first = w.first;
                 const int rg = w.t * kTileRows + row;
                 const float sig = fmaxf(sig_next, 0x1p-100f);
@@ -551,34 +550,40 @@ __global__ void __launch_bounds__(Wide8::THREADS, 1)
                     const float2 d1 = add2(make_float2(x[4 * q + 2], x[4 * q + 3]), make_float2(mm.z, mm.w));
                     over = fmaxf(over, fmaxf(fmaxf(d0.x, d0.y), fmaxf(d1.x, d1.y)));
                 }
-                const bool need = first || !ok || over > C::THRESH + C::PSCALE;
+                const bool need = seen_tiles == look_at || !ok || over > kTopLog2_8;
                 if (named_bar_or(SMX, NSM, need)) {
-                    // ---- some score passes its column's maximum: the tile's maxima, new maxima, O^T rescaled.
-                    // Step 3 of the last tile completes first (the reduction borrows the P^T buffers).
-                    if (k > 0) ok = ok && spin_phase<false>(bar(C::PE), (k - 1) & 1, wc, status);
+                    // ---- the tile's column maxima, m moved where it has to, O^T rescaled
                     if (!named_bar_and(SMX, NSM, ok)) {
                         stop = true;
                         break;
                     }
-                    tc_fence_after();
                     const float wmax = warp_colreduce16<true>(x, lane);
-                    if ((lane & 1) == 0) red[quad * C::NC + 16 * cq + col16(lane)] = wmax;
+                    if ((lane & 1) == 0)
+                        atomicMax(mx_s + (quad >> 1) * C::NC + 16 * cq + col16(lane), ordered_bits(__float_as_int(wmax)));
                     named_bar_sync(SMX, NSM);
-                    bool resc = false;
+                    bool moved = false;
                     if (tid < C::NC) {
-                        const float mt = fmaxf(fmaxf(red[tid], red[C::NC + tid]),
-                                               fmaxf(red[2 * C::NC + tid], red[3 * C::NC + tid]));
-                        const float mo = C::PSCALE - m_s[tid];
-                        float a = 1.f;
-                        if (mt > mo + C::THRESH) {
-                            const float mn = mt + C::HEADROOM;
-                            a = fast_exp2(mo - mn);  // 0 for a column that saw no row so far
-                            m_s[tid] = C::PSCALE - mn;
-                            resc = !first;  // (a first tile's O^T does not exist yet)
+                        const float h0 = __int_as_float(ordered_bits(mx_s[tid]));
+                        const float h1 = __int_as_float(ordered_bits(mx_s[C::NC + tid]));
+                        mx_s[tid] = mx_s[C::NC + tid] = kOrderedLowest;
+                        highest = fmaxf(highest, fmaxf(h0, h1));
+                        const bool look = seen_tiles == look_at;
+                        const float from = m_s[tid], to = follow_maximum8(from, h0, h1, highest, look);
+                        alpha_s[tid] = fast_exp2(to - from);  // 0 for a column that saw no row so far
+                        m_s[tid] = to;
+                        moved = to != from && !first;  // (a first tile's O^T does not exist yet)
+                        if (moved && fmaxf(h0, h1) + from > kTopLog2_8 + kJump8) {
+                            look_at = seen_tiles + 1;
+                            look_gap = kLookStep8;
+                        } else if (look) {
+                            look_at = seen_tiles + look_gap;
+                            look_gap *= kLookStep8;
                         }
-                        alpha_s[tid] = a;
                     }
-                    if (named_bar_or(SMX, NSM, resc)) {
+                    if (named_bar_or(SMX, NSM, moved)) {
+                        // step 3 of the last tile completes first
+                        ok = ok && spin_phase<false>(bar(C::PE), (k - 1) & 1, wc, status);
+                        tc_fence_after();
                         const float *al = alpha_s + 16 * cq;
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
@@ -597,8 +602,8 @@ __global__ void __launch_bounds__(Wide8::THREADS, 1)
                 }
                 sig_next = read_scale(w, next_page);  // in flight until the next tile
                 // ---- P^T: stored 2^(score + log2 s - m + PSCALE), summed as 2^(score - m)
-                const float inv = C::PUNIT / sig;
-                const float2 inv2 = make_float2(inv, inv);
+                const float inv = kPUnit8 / sig;
+                const float2 inv2 = make_float2(inv, inv), dith = make_float2(dither8(row), dither8(row));
                 uint32_t hi[4], lo[4];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
@@ -616,7 +621,8 @@ __global__ void __launch_bounds__(Wide8::THREADS, 1)
                         const uint16_t h = f32x2_to_e4m3x2(pv.x, pv.y);
                         const float2 f = e4m3x2_to_f32x2(h);
                         h2[e] = h;
-                        l2[e] = f32x2_to_e4m3x2(pv.x - f.x, pv.y - f.y);
+                        const float2 rest = add2(pv, dith);
+                        l2[e] = f32x2_to_e4m3x2(rest.x - f.x, rest.y - f.y);
                     }
                     hi[q] = h2[0] | h2[1] << 16;
                     lo[q] = l2[0] | l2[1] << 16;
@@ -653,7 +659,7 @@ __global__ void __launch_bounds__(Wide8::THREADS, 1)
                 l_own = (sums[tid] + sums[C::NC + tid]) + (sums[2 * C::NC + tid] + sums[3 * C::NC + tid]);
             auto finish_column = [&](float mm, float l, float as, float ap) {
                 const bool empty = !(l > 0.f);
-                const float inv = empty ? 0.f : C::PUNIT / l;
+                const float inv = empty ? 0.f : kPUnit8 / l;
                 alpha_s[tid] = as * inv;
                 qv_s[tid] = ap * inv;
                 if (c0 + tid < p.ncols && (mode == 1 || rank == 0)) {
@@ -682,7 +688,7 @@ __global__ void __launch_bounds__(Wide8::THREADS, 1)
             const float4 *fa = reinterpret_cast<const float4 *>(alpha_s + 16 * cq);
             const float4 *fb = reinterpret_cast<const float4 *>(qv_s + 16 * cq);
             if (mode == 1) {
-                if (tid < C::NC) finish_column(C::PSCALE - m_s[tid], l_own, 1.f, 0.f);
+                if (tid < C::NC) finish_column(kPScaleLog2_8 - m_s[tid], l_own, 1.f, 0.f);
                 named_bar_sync(SMX, NSM);
 #pragma unroll 1
                 for (int i = 0; i < 4; ++i) {
@@ -726,7 +732,7 @@ __global__ void __launch_bounds__(Wide8::THREADS, 1)
                 const float4 *xs = reinterpret_cast<const float4 *>(smem + C::OFF_XM);
                 const float *ml = reinterpret_cast<const float *>(smem + C::OFF_XML);
                 if (tid < C::NC) {
-                    const float m = C::PSCALE - m_s[tid], mp = C::PSCALE - ml[tid], lp = ml[C::NC + tid];
+                    const float m = kPScaleLog2_8 - m_s[tid], mp = kPScaleLog2_8 - ml[tid], lp = ml[C::NC + tid];
                     const float mm = fmaxf(m, mp);
                     const float as = fast_exp2(m - mm), ap = fast_exp2(mp - mm);  // 0 for a part without rows
                     // rank 0's term first in both CTAs, so that both compute the same l
