@@ -27,7 +27,9 @@
 //     groups of 128 store one bf16 term, used when every sequence of the batch is long enough
 //     (the plan decides; see plan_core.h).  Tree decodes (TREE) test mask bits in the tiles that
 //     reach into the new rows, and may take groups of 128 with short sequences among them, whose
-//     P is then multiplied as hi and lo in two passes.
+//     P is then multiplied as hi and lo in two passes.  In their groups of 128 the sums of P's terms are taken by
+//     mma.sync (sum_columns8), so that O of one pass can be divided by the sum of what was multiplied: 512 columns at
+//     B=8, 8192..32768 rows 178 -> 189 us for it.
 //
 // Measured, kernel and combine: B=32 h=128, 786 MB: 0.216 ms, 3.6 TB/s, 879 TFLOP/s, 0.56 of the HBM
 // roof; B=16 q_len=4 h=16, 604 MB: 0.144 ms, 4.2 TB/s, 0.64; 256 columns on 32768 rows: 1051 TFLOP/s,
@@ -66,6 +68,7 @@ constexpr uint32_t kDuoCtlLx = 4608;      // float[128] peer's row sums (receive
 constexpr uint32_t kDuoCtlMt = 5120;      // float[128] this CTA's tile maxima / row sums
 constexpr uint32_t kDuoCtlVis = 5632;     // int[128] visible rows per column of the current sequence
 constexpr uint32_t kDuoCtlNm = 6144;      // float[128] minus the running maximum (kNoRow: no row seen yet)
+constexpr uint32_t kDuoCtlLr = 6656;      // float[128] peer's sums of rounded P (received; one-term trees)
 constexpr uint32_t kDuoCtlEnd = 7168;     // data regions start here (1024-aligned)
 constexpr int kDuoThreads = 384;
 constexpr int kDuoMaxSlots = 4;           // slots per operand ring that have barriers
@@ -105,7 +108,7 @@ constexpr uint32_t kDuoSmemAlloc =
 
 template <class C>
 constexpr bool duo_cfg_fits() {
-    return C::BYTES + 1024 <= 232448 && kDuoCtlNm + 512 <= kDuoCtlEnd && C::S_COL + 2 * C::NC <= 512 && C::P_PITCH == 128 &&
+    return C::BYTES + 1024 <= 232448 && kDuoCtlNm + 512 <= kDuoCtlLr && kDuoCtlLr + 512 <= kDuoCtlEnd && C::S_COL + 2 * C::NC <= 512 && C::P_PITCH == 128 &&
            C::NS1 <= kDuoMaxSlots && C::NS3 <= kDuoMaxSlots && C::OFF_Q % 1024 == 0 && C::OFF_P % 1024 == 0 && C::NC <= 128 && C::NH % 16 == 0;
 }
 static_assert(duo_cfg_fits<DuoCfg64>() && duo_cfg_fits<DuoCfg128>(), "shared memory / TMEM plan");
@@ -152,12 +155,30 @@ enum : int {
     kEvEpiO = 40        // epilogue: outputs (or partials) stored
 };
 
+// Adds to acc the column sums of 8 columns of bf16 pairs over the rows (lanes) of a warp, four rows a lane group: lane
+// (g, q) = (lane / 4, lane % 4) gives, as rows g and g + 8 of the 16 x 16 operand, words 0, 2 and 1, 3 of its KV row
+// (places 2q, 2q + 1 and 8 + 2q, 9 + 2q), and the other operand sends places of equal parity and half to one
+// result column each: columns 0..3 of the result for `second` = 0, 4..7 for 1.  So acc[0..3] of lanes with q = 0, 1 are
+// columns 4q .. 4q + 3 of the first eight, with q = 2, 3 those of the second.  (8 instructions a row of 64 columns,
+// instead of 64 additions and as many registers.)
+__device__ __forceinline__ void sum_columns8(float (&acc)[4], const uint32_t (&w)[4], int lane, int second) {
+    const int n = (lane >> 2) - 4 * second;
+    const uint32_t b0 = n == 0 ? 0x3F80u : n == 1 ? 0x3F800000u : 0u, b1 = n == 2 ? 0x3F80u : n == 3 ? 0x3F800000u : 0u;
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(acc[0]), "+f"(acc[1]), "+f"(acc[2]), "+f"(acc[3])
+        : "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(b0), "r"(b1));
+}
+
 template <class C, bool TR, bool TREE>
 __device__ __forceinline__ void duo_body(const DuoMaps &tm, const DecodeParams &p, uint8_t *smem, uint32_t sbase,
                                          uint32_t tmem, uint32_t rank, int unit, int grp, int groups, bool has_work,
                                          volatile WaitCtl *wc, int32_t *status, bool &pv_pending) {
     using BR = DuoBars;
     constexpr int NC = C::NC, NH = C::NH;
+    // One-term groups of a tree decode: O is divided by the sum of P's rounded terms
+    constexpr bool TWO_SUMS = TREE && !C::SPLIT;
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     const uint32_t peer = rank ^ 1u;
@@ -571,6 +592,7 @@ __device__ __forceinline__ void duo_body(const DuoMaps &tm, const DecodeParams &
         float *red = reinterpret_cast<float *>(smem + kDuoCtlRed);
         const float *mx = reinterpret_cast<const float *>(smem + kDuoCtlMx);
         const float *lx = reinterpret_cast<const float *>(smem + kDuoCtlLx);
+        const float *lr = reinterpret_cast<const float *>(smem + kDuoCtlLr);
         float *mt = reinterpret_cast<float *>(smem + kDuoCtlMt);
         int *vis_s = reinterpret_cast<int *>(smem + kDuoCtlVis);
         // the peer's vote number v lands in slot v & 1 (its next vote may arrive before this CTA has read
@@ -586,6 +608,7 @@ __device__ __forceinline__ void duo_body(const DuoMaps &tm, const DecodeParams &
         const uint32_t vote_remote = map_to_rank(sbase + kDuoCtlMisc + 64, peer);
         const uint32_t mx_remote = map_to_rank(sbase + kDuoCtlMx, peer);
         const uint32_t lx_remote = map_to_rank(sbase + kDuoCtlLx, peer);
+        const uint32_t lr_remote = map_to_rank(sbase + kDuoCtlLr, peer);
         bool ok = true, stop = false;
         int k = 0, kv = 0, votes = 0, xmr = 0, xlr = 0;  // units, passes of step 3, votes, exchange rounds
         TraceRowT<TR> tr;
@@ -623,7 +646,11 @@ __device__ __forceinline__ void duo_body(const DuoMaps &tm, const DecodeParams &
         // P^T of this thread's row for its columns, with the final maxima of the unit: into this
         // CTA's buffer (own columns) or the peer's (st.async, counted on its XF barrier); the
         // probabilities are added to lpart.
-        float lpart[NH];
+        float lpart[TWO_SUMS ? 1 : NH];
+        // TWO_SUMS: the sums of P's rounded terms and of what their rounding left, taken over the warp's rows by
+        // matrix instructions whose other operand picks columns (sum_columns8): word i of block c: column
+        // 16 c + 4 (lane % 4) + i of this half, summed over the four rows of the lanes alike in lane / 4.
+        float sum_hi[TWO_SUMS ? NH / 16 : 1][4], sum_lo[TWO_SUMS ? NH / 16 : 1][4];
         // (rest: the term that P_hi's rounding left, for a second pass of step 3)
         auto write_p = [&](bool full, int rg, auto rest) {
 #pragma unroll
@@ -645,19 +672,23 @@ __device__ __forceinline__ void duo_body(const DuoMaps &tm, const DecodeParams &
                                                   e == 0 ? make_float2(nm.x, nm.y) : make_float2(nm.z, nm.w));
                             const float2 pv = make_float2(fast_exp2(d.x), fast_exp2(d.y));
                             const uint32_t h = pack_bf16x2(pv.x, pv.y);
-                            if constexpr (!decltype(rest)::value) {
+                            if constexpr (!decltype(rest)::value) hi[2 * q + e / 2] = h;
+                            if constexpr (!decltype(rest)::value && !TWO_SUMS) {
                                 const float2 l = add2(make_float2(lpart[32 * cc + n], lpart[32 * cc + n + 1]), pv);
                                 lpart[32 * cc + n] = l.x;
                                 lpart[32 * cc + n + 1] = l.y;
-                                hi[2 * q + e / 2] = h;
                             }
-                            if constexpr (C::SPLIT || decltype(rest)::value) {
+                            if constexpr (C::SPLIT || TWO_SUMS || decltype(rest)::value) {
                                 // p - hi, exactly rounded as a subtraction
                                 const float2 r = fma2(make_float2(__uint_as_float(h << 16), __uint_as_float(h & 0xFFFF0000u)),
                                                       make_float2(-1.f, -1.f), pv);
-                                (C::SPLIT ? lo : hi)[2 * q + e / 2] = pack_bf16x2(r.x, r.y);
+                                (decltype(rest)::value && !C::SPLIT ? hi : lo)[2 * q + e / 2] = pack_bf16x2(r.x, r.y);
                             }
                         }
+                    }
+                    if constexpr (TWO_SUMS && !decltype(rest)::value) {
+                        sum_columns8(sum_hi[2 * cc + u / 2], hi, lane, u & 1);
+                        sum_columns8(sum_lo[2 * cc + u / 2], lo, lane, u & 1);
                     }
 #pragma unroll
                     for (int hl = 0; hl < (C::SPLIT ? 2 : 1); ++hl) {
@@ -708,8 +739,15 @@ __device__ __forceinline__ void duo_body(const DuoMaps &tm, const DecodeParams &
                     nm_s[tid] = kNoRow;
                 }
                 named_bar_sync(SMX, NSM);
+                if constexpr (TWO_SUMS) {
 #pragma unroll
-                for (int n = 0; n < NH; ++n) lpart[n] = 0.f;
+                    for (int c = 0; c < NH / 16; ++c)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) sum_hi[c][i] = sum_lo[c][i] = 0.f;
+                } else {
+#pragma unroll
+                    for (int n = 0; n < NH; ++n) lpart[n] = 0.f;
+                }
                 for (int tp = t0; tp < t1 && !stop; ++tp, ++k) {
                     const bool first = tp == t0;
                     ok = ok && spin_phase<false>(bar(BR::SF + (k & 1)), (k >> 1) & 1, wc, status);
@@ -835,8 +873,19 @@ __device__ __forceinline__ void duo_body(const DuoMaps &tm, const DecodeParams &
                                 }
                             }
                             tmem_wait_st();
+                            if constexpr (TWO_SUMS) {
 #pragma unroll
-                            for (int n = 0; n < NH; ++n) lpart[n] *= alpha_s[half * NH + n];
+                                for (int c = 0; c < NH / 16; ++c)
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i) {
+                                        const float a = alpha_s[half * NH + 16 * c + 4 * (lane & 3) + i];
+                                        sum_hi[c][i] *= a;
+                                        sum_lo[c][i] *= a;
+                                    }
+                            } else {
+#pragma unroll
+                                for (int n = 0; n < NH; ++n) lpart[n] *= alpha_s[half * NH + n];
+                            }
                         }
                     }
                     // ---- P^T of this CTA's rows (K-half `rank`) once the previous pass of step 3 released that
@@ -878,20 +927,53 @@ __device__ __forceinline__ void duo_body(const DuoMaps &tm, const DecodeParams &
                 // The column sums are summed and exchanged while the last pass of step 3 runs.
                 const int kl = kv - 1;  // that pass
                 tr.put(kEvSmEpi, kl);
+                // this CTA's sum of column tid over the four lane quadrants (rows of warps that share columns)
+                auto quadrants = [&] { return (red[tid] + red[NC + tid]) + (red[2 * NC + tid] + red[3 * NC + tid]); };
+                float rounded = 0.f;  // TWO_SUMS: column tid's sum of rounded P, of this CTA, then of both
+                if constexpr (TWO_SUMS) {
+                    // every lane's four rows joined with the other seven groups'; lanes 0..3 hold the columns
 #pragma unroll
-                for (int ch = 0; ch < NH / 16; ++ch) {
-                    float v16[16];
+                    for (int c = 0; c < NH / 16; ++c)
 #pragma unroll
-                    for (int n = 0; n < 16; ++n) v16[n] = lpart[16 * ch + n];
-                    const float wsum = warp_colreduce16<false>(v16, lane);
-                    if ((lane & 1) == 0) red[quad * NC + half * NH + 16 * ch + col16(lane)] = wsum;
+                        for (int i = 0; i < 4; ++i) {
+#pragma unroll
+                            for (int d = 4; d <= 16; d <<= 1) {
+                                sum_hi[c][i] += __shfl_xor_sync(0xffffffffu, sum_hi[c][i], d);
+                                sum_lo[c][i] += __shfl_xor_sync(0xffffffffu, sum_lo[c][i], d);
+                            }
+                        }
+                    auto put = [&](const float (&v)[NH / 16][4]) {
+                        if (lane < 4) {
+#pragma unroll
+                            for (int c = 0; c < NH / 16; ++c)
+                                *reinterpret_cast<float4 *>(red + quad * NC + half * NH + 16 * c + 4 * lane) =
+                                    make_float4(v[c][0], v[c][1], v[c][2], v[c][3]);
+                        }
+                        named_bar_sync(SMX, NSM);
+                    };
+                    put(sum_hi);
+                    if (tid < NC) rounded = quadrants();
+                    named_bar_sync(SMX, NSM);
+                    put(sum_lo);
+                } else {
+#pragma unroll
+                    for (int ch = 0; ch < NH / 16; ++ch) {
+                        float v16[16];
+#pragma unroll
+                        for (int n = 0; n < 16; ++n) v16[n] = lpart[16 * ch + n];
+                        const float wsum = warp_colreduce16<false>(v16, lane);
+                        if ((lane & 1) == 0) red[quad * NC + half * NH + 16 * ch + col16(lane)] = wsum;
+                    }
+                    named_bar_sync(SMX, NSM);
                 }
-                named_bar_sync(SMX, NSM);
-                if (tid == 0) mbar_arrive_expect_tx(bar(BR::XL), 4 * NC);
+                if (tid == 0) mbar_arrive_expect_tx(bar(BR::XL), (TWO_SUMS ? 8 : 4) * NC);
                 if (tid < NC) {
-                    const float v = (red[tid] + red[NC + tid]) + (red[2 * NC + tid] + red[3 * NC + tid]);
+                    const float v = TWO_SUMS ? rounded + quadrants() : quadrants();
                     mt[tid] = v;
-                    if (ok) st_async_b32(lx_remote + 4u * tid, __float_as_uint(v), xl_remote);
+                    if (ok) {
+                        st_async_b32(lx_remote + 4u * tid, __float_as_uint(v), xl_remote);
+                        if constexpr (TWO_SUMS) st_async_b32(lr_remote + 4u * tid, __float_as_uint(rounded), xl_remote);
+                    }
                 }
                 ok = ok && spin_phase<true>(bar(BR::XL), xlr & 1, wc, status);
                 ++xlr;
@@ -908,10 +990,15 @@ __device__ __forceinline__ void duo_body(const DuoMaps &tm, const DecodeParams &
                 const int slot = seg_slot;
                 // column sum over both CTAs, rank 0's part first in both (identical values)
                 auto col_l = [&](int c) -> float { return rank == 0 ? mt[c] + lx[c] : lx[c] + mt[c]; };
-                // 1 / l per column (0 for a column that saw no row), once, in the idle alpha area
+                // 1 / l per column (0 for a column that saw no row), once, in the idle alpha area.  TWO_SUMS with one
+                // pass: over the sum of what was multiplied, so that a rounding that many of the column's rows share, or
+                // that the one row has which carries it, cancels; the LSE keeps the sum of P itself.
                 if (tid < NC) {
                     const float l = col_l(tid);
-                    alpha_s[tid] = (!(l > 0.f) || m_s[tid] == -INFINITY) ? 0.f : 1.f / l;
+                    float over = l;
+                    if constexpr (TWO_SUMS)
+                        if (passes == 1) over = rank == 0 ? rounded + lr[tid] : lr[tid] + rounded;
+                    alpha_s[tid] = (!(l > 0.f) || m_s[tid] == -INFINITY) ? 0.f : 1.f / over;
                 }
                 named_bar_sync(SMX, NSM);
                 // 16 columns of latent row d: outputs of an unsplit sequence, else partials

@@ -38,11 +38,12 @@ constexpr int kDuoRows = 256;    // KV rows per unit of the duo kernel = UMMA M 
 constexpr int kDqk = 576;
 constexpr int kDv = 512;
 constexpr int kPage = 64;
-// One bf16 P term is accurate enough when the softmax spreads over many rows: its rounding
-// error in O shrinks like 1/sqrt(rows); at 8192 N(0,1) rows an emulation of the pipeline gives
-// RMSE 1.78e-3 x RMS(O_ref) against the 2e-3 bar (bf16 rounding of O alone takes 1.65e-3).  Where few
-// rows carry the softmax less averages out: with 5 % of the rows scaled x8 it is 2.15e-3 at 8192 rows
-// and 2.10e-3 at 32768, against 1.60e-3 with P as hi + lo.
+// One bf16 P term (half a step: 2^-9 of a power of 2, 1.65e-3 RMS, as much again as O's own rounding) averages out in
+// what many rows share: RMSE of O over its RMS at 8192 / 32768 N(0,1) rows 1.78e-3 / 1.70e-3 against the
+// 2e-3 bar (1.65e-3 with P as hi + lo).  Where few rows carry the softmax their rounding stays: with 5 % of the rows
+// scaled x8, all of a sequence in one range, 2.22e-3 / 2.26e-3.  A tree decode divides O by the sum of the rounded terms
+// instead of P's, which takes that out (1.69e-3 / 1.72e-3); the causal form does not.  Neither helps where values have
+// nothing to do with scores and no mean, so that O is what the rows' weights happen to leave: 2.34e-3.
 constexpr int kSingleP_MinRows = 8192;
 
 // header words (int32) at the start of the workspace
