@@ -266,8 +266,8 @@ MLA_API int mla_cache_extend(const int32_t *seqlens, const int32_t *new_lens, co
  * tokens = 0 does nothing.
  *
  * mla_cache_append_fp8: the same into an E4M3 cache.  kv_scale[slot] receives max|row| / 448 over the
- * row's finite values (1 for a row of zeros, and at least 2^-100), kv8 the codes of row / scale, rounded to
- * nearest even; a value that is not finite becomes the NaN code.
+ * row's finite values (1 for a row of zeros, and at least 2^-100), kv8 the codes of the fp32 quotients
+ * row / scale, rounded to nearest even; a value that is not finite becomes the NaN code.
  */
 MLA_API int mla_cache_append(const void *latent, int64_t latent_stride, const void *norm_weight, float eps,
                              const float *rope_table, int max_pos, int interleaved, const int32_t *positions,

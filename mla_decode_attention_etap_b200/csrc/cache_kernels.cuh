@@ -246,20 +246,21 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
                       pack_bf16x2(x[6], x[7]));
 }
 
-// E4M3 codes of 8 values divided by the row's scale, given its reciprocal (the quotient is off by 2^-23,
-// which moves a code only where it lies that near to the border of two); a value that is not finite
-// becomes the NaN code.
-__device__ __forceinline__ uint2 codes8(const float (&x)[8], float inv) {
+// E4M3 codes of 8 values divided by the row's scale, given its reciprocal too: the product is corrected by its
+// residual, which leaves the quotient rounded once, so that the border between two codes, where quotients
+// of bf16 values do lie, falls as it does for the quotient (8192 rows: 6.8 -> 7.3 us).  A value that
+// is not finite becomes the NaN code.
+__device__ __forceinline__ uint2 codes8(const float (&x)[8], float scale, float inv) {
+    const float2 scale2 = make_float2(scale, scale), inv2 = make_float2(inv, inv);
     uint32_t w[2] = {0u, 0u};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        float y[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const float v = x[2 * i + j];
-            y[j] = fabsf(v) < INFINITY ? v * inv : __uint_as_float(0x7FFFFFFFu);
-        }
-        w[i >> 1] |= (uint32_t)f32x2_to_e4m3x2(y[0], y[1]) << (16 * (i & 1));
+        const float2 v = make_float2(x[2 * i], x[2 * i + 1]);
+        const float2 q = mul2(v, inv2);
+        const float2 y = fma2(fma2(make_float2(-q.x, -q.y), scale2, v), inv2, q);
+        const float nan = __uint_as_float(0x7FFFFFFFu);
+        w[i >> 1] |= (uint32_t)f32x2_to_e4m3x2(fabsf(v.x) < INFINITY ? y.x : nan, fabsf(v.y) < INFINITY ? y.y : nan)
+                     << (16 * (i & 1));
     }
     return make_uint2(w[0], w[1]);
 }
@@ -337,7 +338,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
             for (int k = 0; k < 8; ++k) sum += x0[k] * x0[k] + x1[k] * x1[k];
 #pragma unroll
             for (int d = 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-            const float r = rsqrtf(sum * (1.f / kDv) + p.eps);
+            const float r = __frsqrt_rn(sum * (1.f / kDv) + p.eps);
             float w0[8], w1[8];
             unpack8(__ldg(reinterpret_cast<const uint4 *>(p.norm_weight) + lane), w0);
             unpack8(__ldg(reinterpret_cast<const uint4 *>(p.norm_weight) + 32 + lane), w1);
@@ -366,11 +367,11 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
             const float scale = amax > 0.f ? fmaxf(amax / 448.f, 0x1p-100f) : 1.f;
             const float inv = 1.f / scale;
             uint2 *dst = reinterpret_cast<uint2 *>(p.kv8 + (int64_t)slot * kDqk);
-            dst[lane] = codes8(x0, inv);
-            dst[32 + lane] = codes8(x1, inv);
+            dst[lane] = codes8(x0, scale, inv);
+            dst[32 + lane] = codes8(x1, scale, inv);
             if (lane < 4) {
-                dst[64 + rope_chunk<INTERLEAVED>(lane, 0)] = codes8(ra, inv);
-                dst[64 + rope_chunk<INTERLEAVED>(lane, 1)] = codes8(rb, inv);
+                dst[64 + rope_chunk<INTERLEAVED>(lane, 0)] = codes8(ra, scale, inv);
+                dst[64 + rope_chunk<INTERLEAVED>(lane, 1)] = codes8(rb, scale, inv);
             }
             if (lane == 0) p.kv_scale[slot] = scale;
         } else {
