@@ -609,8 +609,9 @@ def check_append_args(latent, norm_weight, rope_table, positions, slots, kv, sta
         qs = q.shape
         if math.prod(qs) != T * h * D_QK or len(qs) < 2 or qs[-2] != h or qs[-1] != D_QK:
             raise ValueError(f"q: shape {tuple(qs)}, expected [{T}, {h}, {D_QK}] or its tokens as [B, q_len]")
-        stride = q_rope.stride()
-        queries = [q_rope.data_ptr(), stride[0], stride[1], h, _dense(q, "q", torch.bfloat16, home, qs)]
+        stride = q_rope.stride()  # (that of a dimension of one entry may be anything)
+        queries = [q_rope.data_ptr(), stride[0] if T > 1 else 0, stride[1] if h > 1 else 0, h,
+                   _dense(q, "q", torch.bfloat16, home, qs)]
     return ([latent.data_ptr(), latent.stride(0) if T > 1 else D_QK, weight], [table, max_pos], where,
             cache + [math.prod(cache_shape[:-1])], queries + [_status_word(status, home)])
 
