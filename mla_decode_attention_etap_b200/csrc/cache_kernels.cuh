@@ -320,7 +320,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
         const int i = lane & 3;
         const uint4 k0 = __ldg(src + 64 + rope_chunk<INTERLEAVED>(i, 0));
         const uint4 k1 = __ldg(src + 64 + rope_chunk<INTERLEAVED>(i, 1));
-        if (pos < 0 || slot < 0) return;  // padding
+        if (pos < 0 || (slot < 0 && pos < p.max_pos)) return;  // padding, or no cache row wanted
         if (pos >= p.max_pos || slot >= p.cache_rows) {
             if (lane == 0) raise_status(p.status, pos >= p.max_pos ? kStatusInvalid : kStatusBlockTable);
             return;

@@ -1,5 +1,5 @@
-"""GPU test of the E4M3 codes that an append stores: those of the fp32 quotient row / scale, rounded to nearest even
-(as the framework's own quantiser of workloads has them)."""
+"""GPU tests of an append's edges: the E4M3 codes it stores are those of the fp32 quotient row / scale, rounded to
+nearest even (as the framework's own quantiser of workloads has them), and every bad position is reported."""
 
 from __future__ import annotations
 
@@ -54,3 +54,28 @@ def test_codes_at_every_border(exponent):
     off = got != exact
     border = (got + exact) / 2
     assert (np.abs(y - border)[off] <= 2.0 ** -24 * np.abs(y)[off]).all()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("heads", [0, 2])
+def test_a_position_past_the_table_is_reported_without_a_slot_too(heads, fp8):
+    latent = torch.randn(3, 576, device="cuda").bfloat16()
+    kv = torch.zeros(1, 64, 576, dtype=torch.uint8 if fp8 else torch.bfloat16, device="cuda")
+    scale = torch.zeros(1, 64, device="cuda")
+    table = torch.cat([torch.ones(5, 32), torch.zeros(5, 32)], 1).cuda()
+    slots = torch.tensor([-1, -1, 7], dtype=torch.int32, device="cuda")
+    q_rope = torch.randn(3, heads, 64, device="cuda").bfloat16() if heads else None
+    for bad, want in ((4, 0), (5, -1), (2 ** 31 - 1, -1)):
+        positions = torch.tensor([0, bad, 1], dtype=torch.int32, device="cuda")
+        status = torch.zeros(64, dtype=torch.int32, device="cuda")
+        q = torch.zeros(3, heads, 576, dtype=torch.bfloat16, device="cuda") if heads else None
+        front = (latent, None, 0.0, table, True, positions, slots, kv)
+        if fp8:
+            m.mla_cache_append_fp8(*front, scale, status, q_rope=q_rope, q=q)
+        else:
+            m.mla_cache_append(*front, status, q_rope=q_rope, q=q)
+        assert int(status[0]) == want
+        rows = kv.view(-1, 576).float().abs().sum(1)
+        assert rows[7] > 0 and rows.count_nonzero() == 1  # the good token's row and no other
+        if heads:
+            assert (q[1, :, 512:].abs().sum() > 0).item() == (want == 0)
