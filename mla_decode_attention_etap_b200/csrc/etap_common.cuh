@@ -29,23 +29,24 @@ constexpr float kRescaleHeadroom = 24.0f;
 // of 64 is rounded away, while it may hold most of a column's sum (a first row with half of it, say, and thousands of
 // equal ones).  So e follows the largest x of the tiles both ways, and what rounding takes in one row it gives in
 // another:
-//  * A move of e stores the tile's largest x at 2^PSCALE, or at 2^PEAK where it stands PEAK_GAP octaves above the
-//    largest of the tile's other half (its neighbours then need the bits).
-//  * e falls where a row would be stored above 2^TOP.  It rises, in a tile that looks, where the largest is stored
-//    under 2^LOW; O^T and the column sums keep up (fp32: their exponents have room), but never so far that the
-//    largest x seen would be stored REACH octaves above PEAK (what lies that far below it cannot matter) or that
-//    e passes ROOM (row scales go down to 2^-100: the sums of 2^(score - m) stay far from fp32's end).
-//  * A column looks in its second tile, then 4, 16, ... tiles later, and right after a tile whose largest was JUMP
-//    octaves above TOP.
+//  * e falls where a row would be stored above 2^TOP; the tile's largest x is then stored at 2^PSCALE, or at 2^PEAK
+//    where it stands PEAK_GAP octaves above the largest of the tile's other half (its neighbours then need the bits).
+//  * e rises, in a tile that looks, where the largest is stored under 2^LOW: then at 2^PSCALE.  O^T and the column
+//    sums keep up (fp32: their exponents have room), but never so far that the largest x seen would be stored REACH
+//    octaves above PSCALE (what lies that far below it cannot matter) or that e passes ROOM (row scales go
+//    down to 2^-100: the sums of 2^(score - m) stay far from fp32's end).
+//  * A column looks in tiles 1, 5, 21, ... of a segment (one after four times as many), and, after a tile whose largest
+//    was JUMP octaves above TOP, in the next one, unless it has looked in the later half of the tiles so far: then
+//    once it is as far again (so that rows that differ by many octaves from tile to tile do not make it look, and move,
+//    in every one).
 //  * The low term is rounded after adding a part of its step that differs by row (dither8), so that rows of
 //    equal x do not lose alike.
-// Kernel's part of the error of O over its RMS, emulated, the worst of many distributions of 300..32768 rows (one heavy
-// row, one in 128, the first 16th, 5 % of them, falling, rising, 2^5..2^20 above the rest): 2.5e-4, where bf16's
-// rounding of O has 1.65e-3; without the dither 9.6e-4; with a maximum that only rises and stored maxima from 4
-// or 16 to 256: 0.8 and 0.47.
+// The kernel's part of the error of O over its RMS, emulated, the worst of many distributions of 300..32768 rows (one
+// heavy row, 2..64 at random, one in 128, the first 16th, 5 % of them, falling, rising, 2^5..2^20 above the rest):
+// 5.8e-4, where bf16's rounding of O has 1.65e-3; without the dither 9.6e-4; with a maximum that only rises and stored
+// maxima from 4 or 16 to 256: 0.8 and 0.47.
 constexpr float kPScaleLog2_8 = 5.0f, kPUnit8 = 0.03125f, kPeakLog2_8 = 8.0f, kPeakGap8 = 5.0f;
 constexpr float kTopLog2_8 = 8.75f, kLowLog2_8 = 1.0f, kJump8 = 4.0f, kReach8 = 24.0f, kRoom8 = 64.0f;
-constexpr int kLookStep8 = 4;
 
 // Minus the running maximum of a column that has seen no row: far above minus any score, and finite, so
 // that a masked score (-inf) plus it is -inf and any other passes the threshold.
@@ -55,12 +56,23 @@ constexpr float kNoRow = 1e30f;
 // largest seen in the tiles that got here (this one included).  e = kNoRow: no row so far.
 __device__ __forceinline__ float follow_maximum8(float e, float half0, float half1, float highest, bool look) {
     const float mt = fmaxf(half0, half1), at = mt + e;  // `at`: where the tile's largest would be stored
-    const float put = fabsf(half0 - half1) > kPeakGap8 ? kPeakLog2_8 : kPScaleLog2_8;
-    if (at > kTopLog2_8) return put - mt;
+    if (at > kTopLog2_8) return (fabsf(half0 - half1) > kPeakGap8 ? kPeakLog2_8 : kPScaleLog2_8) - mt;
     if (look && at < kLowLog2_8 && mt > -INFINITY)
-        return fmaxf(e, fminf(put - fmaxf(mt, highest - kReach8), kRoom8));
+        return fmaxf(e, fminf(kPScaleLog2_8 - fmaxf(mt, highest - kReach8), kRoom8));
     return e;
 }
+// The tiles of a segment (numbered from 0, the first always) in which a column looks.
+struct Look8 {
+    int at = 0, last = 0;
+    // after tile `tile` was looked at or its largest would have been stored at 2^stored
+    __device__ __forceinline__ void next(int tile, float stored) {
+        if (tile == at) {
+            last = tile;
+            at = 4 * tile + 1;
+        }
+        if (tile > 0 && stored > kTopLog2_8 + kJump8) at = min(at, max(tile + 1, 2 * last + 1));
+    }
+};
 // The part of the low term's step (2^-9 where it is smallest) that row `row` of a 128-row tile adds: evenly spread, and
 // under half a step, so that 0 stays 0.
 __device__ __forceinline__ float dither8(int row) { return ((float)row - 63.5f) * 0x1p-16f; }

@@ -797,12 +797,12 @@ __global__ void __launch_bounds__(320, 1)
 #pragma unroll
                     for (int n = 0; n < NH; ++n) qv[n] = 1.f;
                 }
-                // E4M3: the tiles of the segment in which this thread's columns look, and the largest x of each so far as
-                // looked at (see etap_common.cuh)
-                int seen_tiles = 0, look_at = 0, look_gap = 1;
-                float highest[C::KV8 ? NH : 1];
-#pragma unroll
-                for (int n = 0; n < (C::KV8 ? NH : 1); ++n) highest[n] = -INFINITY;
+                // E4M3: of column `tid` of the group, if there is one (see etap_common.cuh)
+                const int tid = (warp - 2) * 32 + lane;
+                int seen_tiles = 0;
+                Look8 looks;
+                if (tid >= NG) looks.at = -1;
+                float e_col = kNoRow, highest = -INFINITY;
                 for (int t = t0 + toff; t < t1 && !stop; t += C::TSTEP, ++k, ++seen_tiles) {
                     const bool first = (t == t0 + toff);
                     const int pb = k % C::PB;
@@ -912,7 +912,7 @@ __global__ void __launch_bounds__(320, 1)
                         }
                     }
                     // ---- pass 1: full scores of this thread's columns (exchange for CH == 1), scale + mask
-                    bool need = (C::KV8 ? seen_tiles == look_at : first) || !ok;
+                    bool need = (C::KV8 ? seen_tiles == looks.at : first) || !ok;
 #pragma unroll
                     for (int ch = 0; ch < C::CH; ++ch) {
                         float(&x)[8] = xc[ch];
@@ -972,8 +972,7 @@ __global__ void __launch_bounds__(320, 1)
                     }
                     // ---- one vote per tile; the slow path takes the column maxima of all chunks
                     float alpha[C::CH][8];
-                    bool rescale = false, jumped = false;
-                    const bool look = seen_tiles == look_at;  // (E4M3)
+                    bool rescale = false;
 #pragma unroll
                     for (int ch = 0; ch < C::CH; ++ch)
 #pragma unroll
@@ -991,54 +990,62 @@ __global__ void __launch_bounds__(320, 1)
                             if ((lane & 3) == 0) rb[quad * NG + 16 * ch + 8 * half + col8(lane)] = wmax;
                         }
                         named_bar_sync(SMX, NSM);
+                        if constexpr (C::KV8) {
+                            // one thread per column follows its maximum (all threads doing so for their columns costs
+                            // more than the barrier: long code, rarely run)
+                            bool moved = false;
+                            if (tid < NG) {
+                                const float h0 = fmaxf(rb[tid], rb[NG + tid]), h1 = fmaxf(rb[2 * NG + tid], rb[3 * NG + tid]);
+                                highest = fmaxf(highest, fmaxf(h0, h1));
+                                const float from = e_col;
+                                e_col = follow_maximum8(from, h0, h1, highest, seen_tiles == looks.at);
+                                rb[tid] = e_col;
+                                rb[NG + tid] = first ? 1.f : fast_exp2(e_col - from);  // 0: a column without a row so far
+                                moved = e_col != from && !first;  // (a first tile's O^T does not exist yet)
+                                looks.next(seen_tiles, fmaxf(h0, h1) + from);
+                            }
+                            rescale = named_bar_or(SMX, NSM, moved);
 #pragma unroll
-                        for (int ch = 0; ch < C::CH; ++ch) {
+                            for (int ch = 0; ch < C::CH; ++ch)
 #pragma unroll
-                            for (int n4 = 0; n4 < 8; n4 += 4) {
-                                const int c0 = 16 * ch + 8 * half + n4;
-                                const float4 a = *reinterpret_cast<const float4 *>(rb + 0 * NG + c0);
-                                const float4 bq = *reinterpret_cast<const float4 *>(rb + 1 * NG + c0);
-                                const float4 c = *reinterpret_cast<const float4 *>(rb + 2 * NG + c0);
-                                const float4 d = *reinterpret_cast<const float4 *>(rb + 3 * NG + c0);
-                                const float mt4[4] = {fmaxf(fmaxf(a.x, bq.x), fmaxf(c.x, d.x)),
-                                                      fmaxf(fmaxf(a.y, bq.y), fmaxf(c.y, d.y)),
-                                                      fmaxf(fmaxf(a.z, bq.z), fmaxf(c.z, d.z)),
-                                                      fmaxf(fmaxf(a.w, bq.w), fmaxf(c.w, d.w))};
+                                for (int n4 = 0; n4 < 8; n4 += 4) {
+                                    const int c0 = 16 * ch + 8 * half + n4;
+                                    const float4 to = *reinterpret_cast<const float4 *>(rb + c0);
+                                    const float4 by = *reinterpret_cast<const float4 *>(rb + NG + c0);
+                                    const float to4[4] = {to.x, to.y, to.z, to.w}, by4[4] = {by.x, by.y, by.z, by.w};
 #pragma unroll
-                                for (int u = 0; u < 4; ++u) {
-                                    const int n = n4 + u, li = 8 * ch + n;
-                                    if constexpr (C::KV8) {
-                                        const float h0 = fmaxf(u == 0 ? a.x : u == 1 ? a.y : u == 2 ? a.z : a.w,
-                                                               u == 0 ? bq.x : u == 1 ? bq.y : u == 2 ? bq.z : bq.w);
-                                        const float h1 = fmaxf(u == 0 ? c.x : u == 1 ? c.y : u == 2 ? c.z : c.w,
-                                                               u == 0 ? d.x : u == 1 ? d.y : u == 2 ? d.z : d.w);
-                                        highest[li] = fmaxf(highest[li], mt4[u]);
-                                        const float from = m[li] == -INFINITY ? kNoRow : kPScaleLog2_8 - m[li];
-                                        const float to = follow_maximum8(from, h0, h1, highest[li], look);
-                                        if (to != from) {
-                                            m[li] = kPScaleLog2_8 - to;
-                                            if (!first) {  // (a first tile's O^T does not exist yet)
-                                                alpha[ch][n] = fast_exp2(to - from);  // 0: a column without a row so far
-                                                rescale = true;
-                                                jumped = jumped || mt4[u] + from > kTopLog2_8 + kJump8;
-                                            }
+                                    for (int u = 0; u < 4; ++u) {
+                                        m[8 * ch + n4 + u] = to4[u] == kNoRow ? -INFINITY : kPScaleLog2_8 - to4[u];
+                                        alpha[ch][n4 + u] = by4[u];
+                                    }
+                                }
+                        } else {
+#pragma unroll
+                            for (int ch = 0; ch < C::CH; ++ch) {
+#pragma unroll
+                                for (int n4 = 0; n4 < 8; n4 += 4) {
+                                    const int c0 = 16 * ch + 8 * half + n4;
+                                    const float4 a = *reinterpret_cast<const float4 *>(rb + 0 * NG + c0);
+                                    const float4 bq = *reinterpret_cast<const float4 *>(rb + 1 * NG + c0);
+                                    const float4 c = *reinterpret_cast<const float4 *>(rb + 2 * NG + c0);
+                                    const float4 d = *reinterpret_cast<const float4 *>(rb + 3 * NG + c0);
+                                    const float mt4[4] = {fmaxf(fmaxf(a.x, bq.x), fmaxf(c.x, d.x)),
+                                                          fmaxf(fmaxf(a.y, bq.y), fmaxf(c.y, d.y)),
+                                                          fmaxf(fmaxf(a.z, bq.z), fmaxf(c.z, d.z)),
+                                                          fmaxf(fmaxf(a.w, bq.w), fmaxf(c.w, d.w))};
+#pragma unroll
+                                    for (int u = 0; u < 4; ++u) {
+                                        const int n = n4 + u, li = 8 * ch + n;
+                                        if (first) {
+                                            m[li] = mt4[u] + C::HEADROOM;
+                                        } else if (mt4[u] > m[li] + C::THRESH) {
+                                            alpha[ch][n] = fast_exp2(m[li] - (mt4[u] + C::HEADROOM));
+                                            m[li] = mt4[u] + C::HEADROOM;
+                                            rescale = true;
                                         }
-                                    } else if (first) {
-                                        m[li] = mt4[u] + C::HEADROOM;
-                                    } else if (mt4[u] > m[li] + C::THRESH) {
-                                        alpha[ch][n] = fast_exp2(m[li] - (mt4[u] + C::HEADROOM));
-                                        m[li] = mt4[u] + C::HEADROOM;
-                                        rescale = true;
                                     }
                                 }
                             }
-                        }
-                        if (jumped) {
-                            look_at = seen_tiles + 1;
-                            look_gap = kLookStep8;
-                        } else if (look) {
-                            look_at = seen_tiles + look_gap;
-                            look_gap *= kLookStep8;
                         }
                     }
                     // ---- pass 2: probabilities, P^T (hi + lo) into shared memory, O^T rescale

@@ -505,8 +505,10 @@ __global__ void __launch_bounds__(Wide8::THREADS, 1)
                 rq[n] = qv_s[16 * cq + n] * p.scale_log2;
             }
             bool more = true;
-            // the tiles of the segment in which a column (that of this thread, if it has one) looks, see etap_common.cuh
-            int seen_tiles = 0, look_at = tid < C::NC ? 0 : -1, look_gap = 1;
+            // of this thread's column, if it has one (see etap_common.cuh)
+            int seen_tiles = 0;
+            Look8 looks;
+            if (tid >= C::NC) looks.at = -1;
             float highest = -INFINITY;
             for (; more; ++k, ++seen_tiles) {
                 const bool first = w.first;
@@ -550,7 +552,7 @@ __global__ void __launch_bounds__(Wide8::THREADS, 1)
                     const float2 d1 = add2(make_float2(x[4 * q + 2], x[4 * q + 3]), make_float2(mm.z, mm.w));
                     over = fmaxf(over, fmaxf(fmaxf(d0.x, d0.y), fmaxf(d1.x, d1.y)));
                 }
-                const bool need = seen_tiles == look_at || !ok || over > kTopLog2_8;
+                const bool need = seen_tiles == looks.at || !ok || over > kTopLog2_8;
                 if (named_bar_or(SMX, NSM, need)) {
                     // ---- the tile's column maxima, m moved where it has to, O^T rescaled
                     if (!named_bar_and(SMX, NSM, ok)) {
@@ -567,18 +569,12 @@ __global__ void __launch_bounds__(Wide8::THREADS, 1)
                         const float h1 = __int_as_float(ordered_bits(mx_s[C::NC + tid]));
                         mx_s[tid] = mx_s[C::NC + tid] = kOrderedLowest;
                         highest = fmaxf(highest, fmaxf(h0, h1));
-                        const bool look = seen_tiles == look_at;
-                        const float from = m_s[tid], to = follow_maximum8(from, h0, h1, highest, look);
+                        const float from = m_s[tid];
+                        const float to = follow_maximum8(from, h0, h1, highest, seen_tiles == looks.at);
                         alpha_s[tid] = fast_exp2(to - from);  // 0 for a column that saw no row so far
                         m_s[tid] = to;
                         moved = to != from && !first;  // (a first tile's O^T does not exist yet)
-                        if (moved && fmaxf(h0, h1) + from > kTopLog2_8 + kJump8) {
-                            look_at = seen_tiles + 1;
-                            look_gap = kLookStep8;
-                        } else if (look) {
-                            look_at = seen_tiles + look_gap;
-                            look_gap *= kLookStep8;
-                        }
+                        looks.next(seen_tiles, fmaxf(h0, h1) + from);
                     }
                     if (named_bar_or(SMX, NSM, moved)) {
                         // step 3 of the last tile completes first
