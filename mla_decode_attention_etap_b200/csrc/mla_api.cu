@@ -40,7 +40,7 @@ int mla::record_cuda_error(cudaError_t e, const char *what) { return cuda_fail(e
 
 namespace {
 
-bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+using mla::is_aligned;
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
                                   const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
@@ -198,7 +198,10 @@ cudaError_t launch_duo(const mla::DuoMaps &maps, const mla::DecodeParams &p, int
     return cudaLaunchKernelEx(&cfg, mla::etap_duo_kernel<mla::DuoCfg64, mla::DuoCfg128>, maps, p);
 }
 
-// The E4M3 cache's tree decode of more than 16 columns, on the duo kernel's grid.
+// The E4M3 cache's tree decode of more than 16 columns, on the duo kernel's grid.  Its groups of 64 or 128 columns are
+// the faster ones at 17 columns already, although most of them are padding there: B=16, 16384..32768 rows, 24, 32, 64 and 256
+// columns, 80.6, 81, 83 and 230 us against 113, 116, 160 and 466 in the pair kernel's groups of 32 (the causal decode
+// of the same shapes); up to 16 columns the pair kernel takes 86.
 cudaError_t launch_wide8(const CUtensorMap &tm_kv, const CUtensorMap &tm_kvr, const mla::DecodeParams &p, int clusters,
                          cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
@@ -350,7 +353,7 @@ int mla_decode_plan(const int32_t *seqlens, int batch, int q_len, int num_heads,
     int st = check_shape(batch, q_len, num_heads, num_sms);
     if (st != MLA_OK) return st;
     if (!seqlens || !workspace) return MLA_ERR_INVALID_ARG;
-    if (!aligned(seqlens, 4) || !aligned(workspace, 256)) return MLA_ERR_ALIGNMENT;
+    if (!is_aligned(seqlens, 4) || !is_aligned(workspace, 256)) return MLA_ERR_ALIGNMENT;
     const mla::WsLayout lay = mla::ws_layout(batch, q_len, num_heads, num_sms);
     if (workspace_bytes < lay.base) return MLA_ERR_WORKSPACE;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -381,7 +384,7 @@ int mla_combine(void *workspace, int batch, int q_len, int num_heads, int num_sm
     int st = check_shape(batch, q_len, num_heads, num_sms);
     if (st != MLA_OK) return st;
     if (!workspace || !o || !lse) return MLA_ERR_INVALID_ARG;
-    if (!aligned(workspace, 256) || !aligned(o, 16) || !aligned(lse, 4)) return MLA_ERR_ALIGNMENT;
+    if (!is_aligned(workspace, 256) || !is_aligned(o, 16) || !is_aligned(lse, 4)) return MLA_ERR_ALIGNMENT;
     return launch_combine(workspace, batch, q_len, num_heads, num_sms, o, lse, 0, mla::kWaitLimitNs,
                           reinterpret_cast<cudaStream_t>(stream));
 }
@@ -419,12 +422,12 @@ int decode_fwd_impl(const void *q, const void *kv, const float *kv_scale, const 
     if (paged) {
         if (kv_rows % MLA_PAGE_SIZE != 0 || max_blocks < 1) return MLA_ERR_INVALID_ARG;
         if (kv_rows > INT32_MAX) return MLA_ERR_UNSUPPORTED;
-        if (!aligned(block_table, 4)) return MLA_ERR_ALIGNMENT;
+        if (!is_aligned(block_table, 4)) return MLA_ERR_ALIGNMENT;
     } else {
         if ((int64_t)batch * kv_rows > INT32_MAX) return MLA_ERR_UNSUPPORTED;
     }
-    if (!aligned(q, 16) || !aligned(kv, 16) || !aligned(o, 16) || !aligned(lse, 4) || !aligned(seqlens, 4) ||
-        !aligned(workspace, 256) || !aligned(q_lens, 4) || !aligned(kv_scale, 4) || !aligned(tree_mask, 4))
+    if (!is_aligned(q, 16) || !is_aligned(kv, 16) || !is_aligned(o, 16) || !is_aligned(lse, 4) || !is_aligned(seqlens, 4) ||
+        !is_aligned(workspace, 256) || !is_aligned(q_lens, 4) || !is_aligned(kv_scale, 4) || !is_aligned(tree_mask, 4))
         return MLA_ERR_ALIGNMENT;
     const mla::WsLayout lay = mla::ws_layout(batch, q_len, num_heads, num_sms);
     if (workspace_bytes < (tree_mask ? lay.total : lay.base)) return MLA_ERR_WORKSPACE;
@@ -649,7 +652,7 @@ int mla_decode_fwd_trace(const void *q, const void *kv, const int32_t *seqlens, 
                          void *o, float *lse, void *workspace, size_t workspace_bytes, int num_sms,
                          unsigned long long *trace, int trace_cap, void *stream) {
     if (!trace || trace_cap < 1 || trace_cap > (1 << 20)) return MLA_ERR_INVALID_ARG;
-    if (!aligned(trace, 8)) return MLA_ERR_ALIGNMENT;
+    if (!is_aligned(trace, 8)) return MLA_ERR_ALIGNMENT;
     return decode_fwd_impl(q, kv, nullptr, seqlens, nullptr, block_table, batch, q_len, num_heads, kv_rows, max_blocks,
                            softmax_scale, causal, o, lse, workspace, workspace_bytes, num_sms, 0, stream, trace,
                            trace_cap);
@@ -658,7 +661,7 @@ int mla_decode_fwd_trace(const void *q, const void *kv, const int32_t *seqlens, 
 int mla_stream_probe(const void *kv, int64_t rows, int units, int32_t *err, void *stream) {
     if (!kv || !err) return MLA_ERR_INVALID_ARG;
     if (rows < 128 || rows % 128 != 0 || rows > INT32_MAX || units < 1 || units > 4096) return MLA_ERR_INVALID_ARG;
-    if (!aligned(kv, 16) || !aligned(err, 4)) return MLA_ERR_ALIGNMENT;
+    if (!is_aligned(kv, 16) || !is_aligned(err, 4)) return MLA_ERR_ALIGNMENT;
     CUtensorMap tm_kv, tm_kvr;
     int st = encode_rows_576(&tm_kv, kv, (uint64_t)rows, 64);
     if (st != MLA_OK) return st;
@@ -685,7 +688,7 @@ int mla_form_ablation(int form, int heads, int streams, int tiles, int ctas, uns
     if (heads != 16 && heads != 32 && heads != 64 && heads != 128) return MLA_ERR_INVALID_ARG;
     if (streams < 1 || streams > 3 || tiles < 1 || tiles > 65536 || ctas < 1 || ctas > 4096) return MLA_ERR_INVALID_ARG;
     if (!cycles || !err) return MLA_ERR_INVALID_ARG;
-    if (!aligned(cycles, 8) || !aligned(err, 4)) return MLA_ERR_ALIGNMENT;
+    if (!is_aligned(cycles, 8) || !is_aligned(err, 4)) return MLA_ERR_ALIGNMENT;
     static std::once_flag attr_once;
     static cudaError_t attr_err = cudaSuccess;
     std::call_once(attr_once, [] {
@@ -703,7 +706,7 @@ int mla_form_ablation(int form, int heads, int streams, int tiles, int ctas, uns
 
 int mla_decode_read_status(const void *workspace, int *status_out, void *stream) {
     if (!workspace || !status_out) return MLA_ERR_INVALID_ARG;
-    if (!aligned(workspace, 256)) return MLA_ERR_ALIGNMENT;
+    if (!is_aligned(workspace, 256)) return MLA_ERR_ALIGNMENT;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     int32_t v = 0;
     cudaError_t e = cudaMemcpyAsync(&v, workspace, sizeof v, cudaMemcpyDeviceToHost, s);
@@ -739,11 +742,11 @@ int check_static_ws_args(const void *q, const void *kv, const int32_t *seqlens, 
     if (block_table) {
         if (kv_rows % MLA_PAGE_SIZE != 0 || max_blocks < 1) return MLA_ERR_INVALID_ARG;
         if (kv_rows > INT32_MAX) return MLA_ERR_UNSUPPORTED;
-        if (!aligned(block_table, 4)) return MLA_ERR_ALIGNMENT;
+        if (!is_aligned(block_table, 4)) return MLA_ERR_ALIGNMENT;
     } else if ((int64_t)batch * kv_rows > INT32_MAX) {
         return MLA_ERR_UNSUPPORTED;
     }
-    if (!aligned(q, 16) || !aligned(kv, 16) || !aligned(o, 16) || !aligned(lse, 4) || !aligned(seqlens, 4))
+    if (!is_aligned(q, 16) || !is_aligned(kv, 16) || !is_aligned(o, 16) || !is_aligned(lse, 4) || !is_aligned(seqlens, 4))
         return MLA_ERR_ALIGNMENT;
     if (mla::ws_layout(batch, q_len, num_heads, num_sms).base > (size_t)MLA_STATIC_WORKSPACE_BYTES)
         return MLA_ERR_WORKSPACE;
