@@ -39,7 +39,9 @@ struct ExtendParams {
 // together and stored as one; 65536 tokens took 8.2 us with one each and 5.5 us with four), 1 for few
 // (64 tokens of a tree: 3.6 us against 4.9 us, the walks of a thread's tokens running one by one).
 // What bounds it is the chain launch, lengths, sums, barrier, page, stores: 65536 tokens write 0.5 MB, 0.08 us
-// of the measured copy bandwidth.
+// of the measured copy bandwidth.  With parents it is the depth: each token follows its own ancestors, a dependent
+// load a step.  Random trees are shallow (16 x 128 tokens: 8.7 us); chains of 4, 64, 128 tokens in 16 sequences take
+// 3.7, 16 and 62 us, one chain of 1024 tokens 213.  (Times replayed from a graph.)
 template <int TOKENS>
 __global__ void __launch_bounds__(kCacheThreads) extend_kernel(const __grid_constant__ ExtendParams p) {
     __shared__ int64_t scan_smem[32];
@@ -304,9 +306,10 @@ __device__ __forceinline__ void load_angles(const float *table, int pos, int i, 
 // sum of squares is one warp reduction) and two of the rope columns (eight lanes alike), so that the row
 // is read once, kept in registers through norm, rotation and quantisation, and written once.  Queries:
 // four threads per head's 64 columns, each for kQueryHeads heads of one token, with the angles kept in
-// registers across them.  Many tokens are bound by HBM: 4096 with 128 heads move 77 MB in 13.3 us, 5.8 TB/s
-// (0.88 of a copy); 8192 E4M3 rows without queries, 16 MB, take 6.7 us (9.1 with the position waited for
-// before the loads, and a division per value), 64 tokens 2.3 us, most of it launch.
+// registers across them.  Replayed from a graph: many tokens are bound by HBM, 256 ragged sequences of up to 16 with 128
+// heads (half of the 4096 rows padding) move 77 MB in 13.3 us, 5.8 TB/s (0.88 of a copy); 8192 E4M3 rows without
+// queries, 16 MB, take 7.4 us in 1.7 waves (64 registers leave room for 4736 of the 8192 warps; 9.1 with the
+// position waited for before the loads), 64 tokens 2.4 us, most of it launch.
 template <bool FP8, bool INTERLEAVED>
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_constant__ AppendParams p) {
     if ((int)blockIdx.x < p.key_blocks) {

@@ -36,7 +36,8 @@
 // 0.64 of the tensor roof.  Neither is reached: at 64 columns a unit takes 4.1 us, its nine K chunks 3.7
 // (1.3 us from a load's issue to its use, four slots) and the chain P^T, step 3, P^T's release 4.0 (step 3
 // waits 0.7 for its third value pair); deeper rings for both do not fit.  16 softmax warps instead of 8
-// took 152 us instead of 150, at 512 columns 196 instead of 185.  The tensor pipe is 40..50 % busy.
+// took 152 us instead of 150, at 512 columns 196 instead of 185 (these, and the rings' figures below, replayed from a
+// graph).  The tensor pipe is 40..50 % busy.
 //
 // The roles that issue loads and matrix instructions run as whole warps, one elected lane per
 // instruction: a loop run by one lane alone takes 80..130 cycles per instruction, a warp's about 50

@@ -3,7 +3,7 @@
 //
 // Computation as in etap_pair_kernel.cuh's E4M3 configurations: S^T = K Q^T with Q as two E4M3 terms
 // times a power of two per column, P^T as two E4M3 terms of 2^(score + log2 s - m + PSCALE) (s: the row's
-// scale), O^T = V^T P^T, fp32 accumulation.  What differs is the layout, made for 64 columns:
+// scale; m follows the tiles' largest both ways, see etap_common.cuh), O^T = V^T P^T, fp32 accumulation.  What differs is the layout, made for 64 columns:
 //
 //   * A CTA holds whole 128-row tiles (72 KB of codes) and all of its 64 columns' Q (72 KB: [Q_hi; Q_lo]
 //     are the 128 B-operand rows of one N = 128 MMA), so that neither scores nor probabilities cross
@@ -18,8 +18,9 @@
 //     distributed shared memory; in its 128-column groups each takes 64 of the columns and both tiles,
 //     and nothing is merged.
 //
-// B=16, h=16, q_len=4, 16384..32768 rows (230 MB of cache): 81 us with its plan in a row of decodes, 2.8 TB/s (the
-// 32-column groups of the pair kernel: 132..179 us on such shapes).  A tile takes a CTA 2.7 us: 1.5 us of matrix
+// B=16, h=16, q_len=4, 16384..32768 rows (230 MB of cache): 83..84 us with its plan, replayed from a graph at full
+// clock, 2.8 TB/s (90..94 called in a row from Python); 32 columns 81 us.  The 32-column groups of the pair kernel,
+// causal, take 160 and 116 us on these shapes.  A tile takes a CTA 2.7 us: 1.5 us of matrix
 // instructions, but the chain of its loads (1.2 us after a slot comes free), scores (0.5), softmax (2.0) and
 // step 3 (1.25) runs over a ring of two tiles; shared memory and TMEM are full.
 //

@@ -82,7 +82,7 @@ MLA_HD int duo_mode(int ncols, int min_len) { return duo_mode1_possible(ncols) &
 // The grouping of the tree schedule: for more than 64 columns groups of 128 wherever the duo schedule takes them, and when every work
 // unit of that grouping gets a unit of KV rows (`units` of kDuoRows in all).  Batches of 16 ragged trees of
 // up to 16 tokens, 16 heads, lengths drawn from 1 to 32768 (three draws each): 194..224 us in groups of
-// 128, 224..269 us in groups of 64.
+// 128, 224..269 us in groups of 64 (replayed from a graph, on the kernel of that time).
 MLA_HD int tree_mode(int ncols, int min_len, int64_t units, int num_sms) {
     if (!duo_mode1_possible(ncols)) return 0;
     return duo_mode(ncols, min_len) || units >= num_ctas(num_sms, duo_groups(ncols, 1)) ? 1 : 0;

@@ -20,7 +20,8 @@ namespace mla {
 // `sched`: 0 pair, 1 duo, 2 tree.  A tree schedule of 64-column groups counts 4: its E4M3 kernel then takes
 // 2.7 us a unit (B=16, 64 columns, 16384..32768 rows: 85.3 us with 2, 81.5 with 4; the bf16 kernel, 32768
 // rows, 152 and 150.5).  With no more units than work units it counts none, so that no work unit gets two
-// (one sequence of 1024 rows, 128 columns: 24.9 us, 23.3 without).
+// (one sequence of 1024 rows, 128 columns: 24.9 us, 23.3 without).  (Plan, decode and combine replayed from a graph,
+// on the kernels of that time; one shape each.)
 MLA_HD int end_cost_units(int sched, int mode, int64_t total, int ctas) {
     if (sched == 2) return total <= ctas ? 0 : mode ? 2 : 4;
     return sched == 0 ? 4 : 2;
