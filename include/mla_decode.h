@@ -127,7 +127,10 @@ MLA_API int mla_decode_plan(const int32_t *seqlens, int batch, int q_len, int nu
  *   causal       0 or 1 (see the header comment)
  *   o            bf16 [batch, q_len, num_heads, 512], 16-byte aligned
  *   lse          fp32 [batch, q_len, num_heads], 4-byte aligned
- *   workspace    the buffer mla_decode_plan filled for the same seqlens and shape
+ *   workspace    the buffer mla_decode_plan filled for the same seqlens, shape and num_sms. A plan whose tables
+ *                lie elsewhere (another shape or num_sms, none at all, or, for a tree decode, one made in a
+ *                workspace too small for its tables) is not used: MLA_ERR_INVALID_ARG is set in the status
+ *                word and the outputs stay as they are. The same holds for mla_combine.
  * Rows of the cache past L_b may hold anything (NaN included): they are masked
  * out and never multiply into O.
  */

@@ -160,8 +160,8 @@ enum : int {
 // (g, q) = (lane / 4, lane % 4) gives, as rows g and g + 8 of the 16 x 16 operand, words 0, 2 and 1, 3 of its KV row
 // (places 2q, 2q + 1 and 8 + 2q, 9 + 2q), and the other operand sends places of equal parity and half to one
 // result column each: columns 0..3 of the result for `second` = 0, 4..7 for 1.  So acc[0..3] of lanes with q = 0, 1 are
-// columns 4q .. 4q + 3 of the first eight, with q = 2, 3 those of the second.  (8 instructions a row of 64 columns,
-// instead of 64 additions and as many registers.)
+// columns 4q .. 4q + 3 of the first eight, with q = 2, 3 those of the second.  (8 instructions for 64 columns of a
+// warp's rows, instead of 64 additions and as many registers a thread.)
 __device__ __forceinline__ void sum_columns8(float (&acc)[4], const uint32_t (&w)[4], int lane, int second) {
     const int n = (lane >> 2) - 4 * second;
     const uint32_t b0 = n == 0 ? 0x3F80u : n == 1 ? 0x3F800000u : 0u, b1 = n == 2 ? 0x3F80u : n == 3 ? 0x3F800000u : 0u;
